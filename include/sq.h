@@ -413,6 +413,117 @@ sq_status sq_w8a8_linear_noalloc(const int8_t* xq, const float* x_scale, const i
                                  const float* w_scale, const void* bias_f16, void* y_f16,
                                  int64_t M, int64_t N, int64_t K, sq_stream_t stream);
 
+/*
+ * 4-bit weights with group scales, for layers whose time is the weight's
+ * bytes (the decoding stage): half the bytes of the INT8 weight, fp16
+ * activations.
+ *   W[n, k] = (q[n, k] - z[n, g]) * s[n, g],   g = k / group
+ * with codes q in 0..15, a fp16 scale s and a zero point z in 0..15 (z = 8
+ * without zero points).  group is 32, 64 or 128; the last group of a row may
+ * be short.  Codes, scales and zero points live together in one packed buffer
+ * of sq_w4_packed_bytes bytes, laid out once for the kernels (read it back
+ * with sq_w4_dequantize); several experts' weights of one shape follow each
+ * other in one buffer.
+ */
+
+/* Bytes of one packed weight (0 for a shape no entry point takes). */
+size_t sq_w4_packed_bytes(int64_t N, int64_t K, int group, int has_zero);
+
+/*
+ * Quantize an fp16 weight (folded by s on the fly when given, exactly as in
+ * sq_quantize_weight: w' = fp16(fp32(w) * s_k)) in groups of a row.  Without zero points:
+ *   s = fp16( r8( max|w'| / 7 ) ),  q = clamp(rint(w' / s), -7, 7) + 8
+ * with zero points, lo = min(w', 0), hi = max(w', 0):
+ *   s = fp16( r7( (hi - lo) / 15 ) ),  z = min(rint(-lo / s), 15),
+ *   q = clamp(rint(w' / s) + z, 0, 15)
+ * where r8 / r7 round to 8 / 7 significant bits, so that every (q - z) * s is
+ * exactly an fp16 number.  A group of zeros gets scale 0; a NaN never sets a
+ * range and is coded as zero; an Inf gives scale Inf (its group's values are
+ * then NaN).
+ *   w fp16 [N, K]; s fp32 [K] or NULL; w4: the packed buffer
+ */
+sq_status sq_quantize_weight_w4(const void* w_f16, int64_t N, int64_t K, const float* s, int group, int has_zero,
+                                void* w4, sq_stream_t stream);
+
+/* Pack codes a caller already has (from another quantizer or a checkpoint).
+ *   codes uint8 [N, K], the low four bits count; scales fp16 [N, ceil(K / group)];
+ *   zeros uint8 [N, ceil(K / group)] or NULL (z = 8, a weight without zero points) */
+sq_status sq_w4_pack(const uint8_t* codes, const void* scales_f16, const uint8_t* zeros, int64_t N, int64_t K,
+                     int group, void* w4, sq_stream_t stream);
+
+/* The values of a packed weight, w_out fp16 [N, K] = fp16((q - z) * s). */
+sq_status sq_w4_dequantize(const void* w4, int64_t N, int64_t K, int group, int has_zero, void* w_out_f16,
+                           sq_stream_t stream);
+
+/*
+ * The linear with a packed 4-bit weight, any number of tokens:
+ *   y[m, n] = fp16( sum_k x[m, k] * W[n, k] + fp32(bias[n]) ),  max(., 0) before the
+ * rounding when relu (a NaN becomes 0).  Sums are fp32.  Needs no workspace;
+ * the same inputs give the same bits on every call.
+ *   x fp16 [M, ldx], ldx >= K, ldx % 8 == 0; bias fp16 [N] or NULL; y fp16 [M, N]
+ */
+sq_status sq_w4a16_linear(const void* x_f16, int64_t M, int64_t ldx, const void* w4, int64_t N, int64_t K, int group,
+                          int has_zero, const void* bias_f16, int relu, void* y_f16, sq_stream_t stream);
+
+/*
+ * Mixture-of-experts layers on packed 4-bit weights: route every token to
+ * topk experts, sort the (token, slot) pairs by expert, run each expert on
+ * its pairs, add a token's results up.  Pair t * topk + j is slot j of token t.
+ */
+#define SQ_MOE_MAX_EXPERTS 512
+#define SQ_MOE_MAX_TOPK 32
+
+/*
+ * Routing.  p = softmax(logits[t, :]), or sigmoid(logits) with sigmoid != 0;
+ * choice c = p + bias (bias NULL: c = p).  With topk_group < n_group the
+ * experts form n_group groups of E / n_group neighbours, a group's score is the sum of its
+ * group_top (1 or 2) largest choices, and only the topk_group groups of the
+ * largest scores stay.  ids[t, :] are the topk experts of the largest choices
+ * among those that stay, largest first, ties to the lowest index (groups too);
+ *   weights[t, j] = p * scale,  p divided first by the sum of the token's
+ * chosen p when renormalize.  Scores are formed and compared in 64 bits.
+ * An expert whose logit is -Inf or NaN (or whose choice is) is masked: it has
+ * score 0 and is never chosen; slots that no expert is left for get id -1 and
+ * weight 0.
+ *   logits fp32 [T, ld], or fp16 with logits_f16 != 0, ld >= E; bias fp32 [E] or NULL;
+ *   ids int32 [T, topk]; weights fp32 [T, topk]; n_group <= 32 divides E
+ */
+sq_status sq_moe_route(const void* logits, int logits_f16, int64_t T, int64_t E, int64_t ld, const float* bias,
+                       int sigmoid, int n_group, int topk_group, int group_top, int topk, int renormalize, float scale,
+                       int32_t* ids, float* weights, sq_stream_t stream);
+
+/*
+ * The pairs sorted by expert: order[offsets[e] .. offsets[e + 1]) are the
+ * pairs with ids[pair] == e, ascending.  Pairs whose id is not in 0 .. E - 1
+ * are left out; the rest of order is -1.
+ *   ids int32 [pairs]; offsets int32 [E + 1]; order int32 [pairs];
+ *   workspace: sq_moe_plan_workspace_bytes(pairs, E) bytes (0 for few pairs; any contents;
+ *   calls that overlap on the GPU need one each)
+ */
+size_t sq_moe_plan_workspace_bytes(int64_t pairs, int64_t E);
+sq_status sq_moe_plan(const int32_t* ids, int64_t pairs, int64_t E, int32_t* offsets, int32_t* order, void* workspace,
+                      size_t ws_bytes, sq_stream_t stream);
+
+/*
+ * The experts' products: for every pair p that the plan lists under expert e,
+ *   y[p, :] = x[p / pairs_per_row, :] W_e^T + bias[e, :]  (ReLU as in sq_w4a16_linear)
+ * pairs_per_row is topk for the product on the tokens and 1 for one on an
+ * earlier product's rows.  Rows of pairs that the plan leaves out are left as
+ * they were.  Plan entries outside [0, pairs) are skipped.
+ *   x fp16 [rows, ldx]; w4: E packed weights; bias fp16 [E, N] or NULL;
+ *   y fp16 [pairs, N], or fp32 with y_f32 != 0
+ */
+sq_status sq_w4a16_experts(const void* x_f16, int64_t rows, int64_t ldx, const void* w4, int64_t E, int64_t N,
+                           int64_t K, int group, int has_zero, const void* bias_f16, int relu,
+                           const int32_t* offsets, const int32_t* order, int64_t pairs, int64_t pairs_per_row,
+                           void* y, int y_f32, sq_stream_t stream);
+
+/* y[t, :] = fp16( sum_j weights[t, j] * y_pairs[t * topk + j, :] ), j ascending, in fp32; slots
+ * whose id is not in 0 .. E - 1 are skipped, their rows are not read.
+ *   y_pairs fp16 [T * topk, N], or fp32 with pairs_f32 != 0; y fp16 [T, N] */
+sq_status sq_moe_combine(const void* y_pairs, int pairs_f32, const int32_t* ids, const float* weights, int64_t T,
+                         int64_t topk, int64_t N, int64_t E, void* y_f16, sq_stream_t stream);
+
 /* Synchronizes `stream`, then reports and clears the current device's status
  * word: SQ_ERR_TIMEOUT if a bounded device wait ran out since the last poll,
  * SQ_ERR_CUDA if the stream reported an error, else SQ_OK. */

@@ -30,6 +30,9 @@ __all__ = [
     "LEVELS", "sq_w8a8_linear_quant", "sq_w8a8_linear_quant_dyn", "sq_w8a8_linear_quant_dyn_workspace_bytes",
     "new_quant_dyn_workspace", "sq_w8a8_bmm", "sq_row_ranges", "sq_quantize_rows_ranged",
     "sq_dequant",
+    "W4Weight", "new_w4_weight", "sq_w4_packed_bytes", "sq_quantize_weight_w4", "sq_w4_pack", "sq_w4_dequantize",
+    "sq_w4a16_linear", "sq_moe_route", "sq_moe_plan", "sq_moe_plan_workspace_bytes", "sq_w4a16_experts",
+    "sq_moe_combine", "W4Linear", "W4Experts", "MOE_MAX_EXPERTS", "MOE_MAX_TOPK",
     "PATH_AUTO", "PATH_TILED", "PATH_SPLITK", "PATH_PAIR", "SPLITK_MAX_M", "DECODE_MAX_M", "MAX_K", "library_path",
 ]
 
@@ -81,6 +84,16 @@ def _load() -> ctypes.CDLL:
         "sq_row_ranges": ([P, I, I, I, P, P, P, P, F, P, P], S),
         "sq_quantize_rows_ranged": ([P, I, I, I, P, P, P, P, F, P, P, P, P], S),
         "sq_dequant": ([P, P, P, P, P, I, I, P], S),
+        "sq_w4_packed_bytes": ([I, I, S, S], Z),
+        "sq_quantize_weight_w4": ([P, I, I, P, S, S, P, P], S),
+        "sq_w4_pack": ([P, P, P, I, I, S, P, P], S),
+        "sq_w4_dequantize": ([P, I, I, S, S, P, P], S),
+        "sq_w4a16_linear": ([P, I, I, P, I, I, S, S, P, S, P, P], S),
+        "sq_moe_route": ([P, S, I, I, I, P, S, S, S, S, S, S, F, P, P, P], S),
+        "sq_moe_plan_workspace_bytes": ([I, I], Z),
+        "sq_moe_plan": ([P, I, I, P, P, P, Z, P], S),
+        "sq_w4a16_experts": ([P, I, I, P, I, I, I, S, S, P, S, P, P, I, I, P, S, P], S),
+        "sq_moe_combine": ([P, S, P, P, I, I, I, I, P, P], S),
         "sq_poll_status": ([P], S),
         "sq_set_wait_budget_ns": ([ctypes.c_uint64], None),
         "sq_selftest_wait_timeout": ([ctypes.c_uint64, P], S),
@@ -598,3 +611,8 @@ class SmoothQuantLinear:
         return y
 
     __call__ = forward
+
+
+from .w4 import (MOE_MAX_EXPERTS, MOE_MAX_TOPK, W4Experts, W4Linear, W4Weight, new_w4_weight,  # noqa: E402
+                 sq_moe_combine, sq_moe_plan, sq_moe_plan_workspace_bytes, sq_moe_route, sq_quantize_weight_w4,
+                 sq_w4_dequantize, sq_w4_pack, sq_w4_packed_bytes, sq_w4a16_experts, sq_w4a16_linear)

@@ -1,0 +1,359 @@
+// k_moe.cu -- routing of tokens to experts: scores and selection, the
+// (token, expert) pairs sorted by expert, and the weighted sum of the
+// experts' outputs.
+#include "sq_ptx.cuh"
+#include "sq_w4.h"
+
+namespace sq {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kRouteWarps = 4;
+constexpr int kMaxV = 16;  // scores a lane holds: up to 512 experts
+
+__device__ __forceinline__ double neg_inf() { return __longlong_as_double(0xfff0000000000000ll); }
+
+// The largest value of the warp and the lowest index among its holders; every
+// lane gets both.
+__device__ __forceinline__ void warp_argmax(double& v, int& i) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const double ov = __shfl_xor_sync(kAll, v, o);
+    const int oi = __shfl_xor_sync(kAll, i, o);
+    if (ov > v || (ov == v && oi < i)) {
+      v = ov;
+      i = oi;
+    }
+  }
+}
+
+// One warp per token; lane l holds experts 32 v + l.  Scores are formed in
+// 64 bits: which experts a token goes to must not hang on the last bits of a
+// 32-bit exponential, and two choices may lie arbitrarily close.
+template <int V>
+__global__ void __launch_bounds__(kRouteWarps * 32) k_moe_route(const RouteArgs a) {
+  extern __shared__ double sh[];  // [warps][E] choices, used for group scores
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_wait();
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
+  if (t >= a.T) return;
+  const int E = a.E;
+
+  double p[V], choice[V];
+  float l[V];
+  float top = -INFINITY;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = 32 * v + lane;
+    l[v] = -INFINITY;
+    if (e < E) {
+      l[v] = a.half ? __half2float(static_cast<const __half*>(a.logits)[t * a.ld + e])
+                    : static_cast<const float*>(a.logits)[t * a.ld + e];
+      if (isnan(l[v])) l[v] = -INFINITY;  // masked, like -inf
+    }
+    top = fmaxf(top, l[v]);
+  }
+  if (a.sigmoid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] = 1.0 / (1.0 + exp(-static_cast<double>(l[v])));
+  } else {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    double sum = 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      // equal to the maximum first: an infinite maximum has score one, not NaN
+      p[v] = l[v] == -INFINITY ? 0.0 : l[v] == top ? 1.0 : exp(static_cast<double>(l[v]) - static_cast<double>(top));
+      sum += p[v];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if (sum > 0.0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) p[v] /= sum;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = 32 * v + lane;
+    choice[v] = neg_inf();
+    if (e < E && l[v] != -INFINITY) {
+      choice[v] = a.bias ? p[v] + static_cast<double>(a.bias[e]) : p[v];
+      if (isnan(choice[v])) choice[v] = neg_inf();
+    }
+  }
+
+  if (a.topk_group < a.n_group) {
+    double* c = sh + warp * E;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (32 * v + lane < E) c[32 * v + lane] = choice[v];
+    __syncwarp();
+    const int per = E / a.n_group;
+    double score = neg_inf();
+    if (lane < a.n_group) {
+      double first = neg_inf(), second = neg_inf();
+      for (int i = 0; i < per; ++i) {
+        const double x = c[lane * per + i];
+        if (x > first) {
+          second = first;
+          first = x;
+        } else if (x > second) {
+          second = x;
+        }
+      }
+      score = a.group_top == 2 && second > neg_inf() ? first + second : first;
+      if (isnan(score)) score = neg_inf();
+    }
+    unsigned keep = 0;
+    for (int j = 0; j < a.topk_group; ++j) {
+      double best = score;
+      int which = lane;
+      warp_argmax(best, which);
+      if (best == neg_inf()) break;
+      keep |= 1u << which;
+      if (lane == which) score = neg_inf();
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = 32 * v + lane;
+      if (e < E && !(keep >> (e / per) & 1u)) choice[v] = neg_inf();
+    }
+  }
+
+  // topk rounds of the warp's largest choice; lane j keeps the j-th expert
+  int my_id = -1;
+  double my_p = 0.0, chosen = 0.0;
+  for (int j = 0; j < a.topk; ++j) {
+    double best = neg_inf();
+    int which = 0x7fffffff;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (choice[v] > best) {
+        best = choice[v];
+        which = 32 * v + lane;
+      }
+    warp_argmax(best, which);
+    if (best == neg_inf()) break;
+    double score = 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (32 * v + lane == which) {
+        choice[v] = neg_inf();
+        score = p[v];
+      }
+    score = __shfl_sync(kAll, score, which & 31);
+    chosen += score;
+    if (lane == j) {
+      my_id = which;
+      my_p = score;
+    }
+  }
+  if (lane < a.topk) {
+    double w = my_p;
+    if (a.renormalize) w = chosen > 0.0 ? w / chosen : 0.0;
+    a.ids[t * a.topk + lane] = my_id;
+    a.weights[t * a.topk + lane] = static_cast<float>(w * a.scale);
+  }
+}
+
+// ------------------------------------------------------------------ plan ----
+constexpr int kPlanThreads = 256;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanChunk = 2048;  // pairs per CTA
+constexpr int kPerWarp = kPlanChunk / kPlanWarps;
+
+__global__ void __launch_bounds__(kPlanThreads)
+    k_plan_count(const int32_t* __restrict__ ids, int64_t P, int E, int32_t* __restrict__ counts) {
+  extern __shared__ int32_t hist[];
+  griddep_wait();
+  for (int e = threadIdx.x; e < E; e += kPlanThreads) hist[e] = 0;
+  __syncthreads();
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * kPlanChunk;
+  for (int i = threadIdx.x; i < kPlanChunk && base + i < P; i += kPlanThreads) {
+    const int e = ids[base + i];
+    if (e >= 0 && e < E) atomicAdd(&hist[e], 1);  // integer counts: any order gives the same
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kPlanThreads) counts[static_cast<int64_t>(blockIdx.x) * E + e] = hist[e];
+}
+
+// A stable counting sort of one chunk: counts per warp and expert, a scan
+// over experts, then every warp places its pairs in their order.  With more
+// than one chunk `counts` holds every chunk's histogram.
+__global__ void __launch_bounds__(kPlanThreads)
+    k_plan_place(const int32_t* __restrict__ ids, int64_t P, int E, const int32_t* __restrict__ counts, int chunks,
+                 int32_t* __restrict__ offsets, int32_t* __restrict__ order) {
+  extern __shared__ int32_t sh32[];
+  int32_t* wcount = sh32;                  // [warps][E]
+  int32_t* total = sh32 + kPlanWarps * E;  // [E + 1]: pairs of all chunks, then their exclusive scan
+  int32_t* base = total + E + 1;           // [E]: pairs of the chunks before this one
+  __shared__ int32_t carry[kPlanWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_wait();
+  for (int i = tid; i < kPlanWarps * E; i += kPlanThreads) wcount[i] = 0;
+  __syncthreads();
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanChunk + warp * kPerWarp;
+  int32_t mine[kPerWarp / 32];
+#pragma unroll
+  for (int i = 0; i < kPerWarp / 32; ++i) {
+    const int64_t q = first + 32 * i + lane;
+    mine[i] = q < P ? ids[q] : -1;
+    if (mine[i] >= E) mine[i] = -1;
+    if (mine[i] >= 0) atomicAdd(&wcount[warp * E + mine[i]], 1);
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += kPlanThreads) {
+    int32_t here = 0;
+    for (int w = 0; w < kPlanWarps; ++w) {
+      const int32_t n = wcount[w * E + e];
+      wcount[w * E + e] = here;  // pairs of this chunk's earlier warps
+      here += n;
+    }
+    int32_t before = 0, all = here;
+    if (chunks > 1) {
+      all = 0;
+      for (int c = 0; c < chunks; ++c) {
+        const int32_t n = counts[static_cast<int64_t>(c) * E + e];
+        if (c < static_cast<int>(blockIdx.x)) before += n;
+        all += n;
+      }
+    }
+    total[e] = all;
+    base[e] = before;
+  }
+  __syncthreads();
+  // exclusive scan of total[0 .. E) in place, E <= 2 * kPlanThreads
+  int32_t a0 = 2 * tid < E ? total[2 * tid] : 0, a1 = 2 * tid + 1 < E ? total[2 * tid + 1] : 0;
+  int32_t inc = a0 + a1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t up = __shfl_up_sync(kAll, inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 31) carry[warp] = inc;
+  __syncthreads();
+  int32_t pre = 0;
+  for (int w = 0; w < warp; ++w) pre += carry[w];
+  const int32_t ex = pre + inc - a0 - a1;
+  if (2 * tid < E) total[2 * tid] = ex;
+  if (2 * tid + 1 < E) total[2 * tid + 1] = ex + a0;
+  if (tid == kPlanThreads - 1) total[E] = pre + inc;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = tid; e <= E; e += kPlanThreads) offsets[e] = total[e];
+  for (int e = tid; e < E; e += kPlanThreads)
+    for (int w = 0; w < kPlanWarps; ++w) wcount[w * E + e] += total[e] + base[e];
+  // entries past the last routed pair
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * kPlanChunk + tid; q < P && q < static_cast<int64_t>(blockIdx.x + 1) * kPlanChunk;
+       q += kPlanThreads)
+    if (q >= total[E]) order[q] = -1;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kPerWarp / 32; ++i) {
+    const int e = mine[i];
+    const unsigned same = __match_any_sync(kAll, e);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    int32_t at = 0;
+    if (e >= 0) at = wcount[warp * E + e];
+    __syncwarp();
+    if (e >= 0) {
+      if (rank == 0) wcount[warp * E + e] = at + __popc(same);
+      order[at + rank] = static_cast<int32_t>(first + 32 * i + lane);
+    }
+    __syncwarp();
+  }
+}
+
+// --------------------------------------------------------------- combine ----
+// y[t] = sum_j weights[t, j] * row (t, j), j ascending, fp32; VEC columns per thread.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256)
+    k_moe_combine(const T* __restrict__ rows, const int32_t* __restrict__ ids, const float* __restrict__ weights,
+                  int64_t T_, int topk, int64_t N, int E, __half* __restrict__ y) {
+  griddep_wait();
+  const int64_t per = N / VEC;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= T_ * per) return;
+  const int64_t t = i / per, n = (i - t * per) * VEC;
+  float acc[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) acc[v] = 0.0f;
+  for (int j = 0; j < topk; ++j) {
+    const int e = ids[t * topk + j];
+    if (e < 0 || e >= E) continue;  // no expert took this pair: its row was never written
+    const float w = weights[t * topk + j];
+    const T* row = rows + (t * topk + j) * N + n;
+    T v[VEC];
+    if constexpr (VEC == 4 && sizeof(T) == 4)
+      *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(row);
+    else if constexpr (VEC == 4)
+      *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(row);
+    else
+      v[0] = row[0];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) acc[k] = __fmaf_rn(w, static_cast<float>(v[k]), acc[k]);
+  }
+  __half out[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) out[v] = __float2half_rn(acc[v]);
+  if constexpr (VEC == 4)
+    *reinterpret_cast<uint2*>(y + t * N + n) = *reinterpret_cast<const uint2*>(out);
+  else
+    y[t * N + n] = out[0];
+}
+
+template <int V>
+cudaError_t route(const RouteArgs& a, const Ctx& c) {
+  const size_t smem = a.topk_group < a.n_group ? sizeof(double) * kRouteWarps * a.E : 0;
+  const int64_t blocks = (a.T + kRouteWarps - 1) / kRouteWarps;
+  return launch_pdl(k_moe_route<V>, dim3(static_cast<unsigned>(blocks)), dim3(kRouteWarps * 32), smem, c.stream, a);
+}
+
+template <typename T>
+cudaError_t combine(const T* rows, const int32_t* ids, const float* weights, int64_t tokens, int topk, int64_t N,
+                    int E, __half* y, const Ctx& c) {
+  const int vec = N % 4 == 0 ? 4 : 1;
+  const int64_t n = tokens * (N / vec);
+  const unsigned blocks = static_cast<unsigned>((n + 255) / 256);
+  if (vec == 4)
+    return launch_pdl(k_moe_combine<T, 4>, dim3(blocks), dim3(256), 0, c.stream, rows, ids, weights, tokens, topk, N,
+                      E, y);
+  return launch_pdl(k_moe_combine<T, 1>, dim3(blocks), dim3(256), 0, c.stream, rows, ids, weights, tokens, topk, N,
+                    E, y);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_route(const RouteArgs& a, const Ctx& c) {
+  if (a.E <= 32) return route<1>(a, c);
+  if (a.E <= 64) return route<2>(a, c);
+  if (a.E <= 128) return route<4>(a, c);
+  if (a.E <= 256) return route<8>(a, c);
+  return route<kMaxV>(a, c);
+}
+
+size_t moe_plan_workspace_bytes(int64_t P, int E) {
+  const int64_t chunks = (P + kPlanChunk - 1) / kPlanChunk;
+  return chunks > 1 ? static_cast<size_t>(chunks) * E * sizeof(int32_t) : 0;
+}
+
+cudaError_t launch_moe_plan(const int32_t* ids, int64_t P, int E, int32_t* offsets, int32_t* order, int32_t* ws,
+                            const Ctx& c) {
+  const int chunks = static_cast<int>((P + kPlanChunk - 1) / kPlanChunk);
+  if (chunks > 1) {
+    const cudaError_t e = launch_pdl(k_plan_count, dim3(chunks), dim3(kPlanThreads), sizeof(int32_t) * E, c.stream,
+                                     ids, P, E, ws);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(k_plan_place, dim3(chunks), dim3(kPlanThreads), sizeof(int32_t) * ((kPlanWarps + 2) * E + 1),
+                    c.stream, ids, P, E, static_cast<const int32_t*>(ws), chunks, offsets, order);
+}
+
+cudaError_t launch_moe_combine(const __half* y16, const float* y32, const int32_t* ids, const float* weights,
+                               int64_t T, int topk, int64_t N, int E, __half* y, const Ctx& c) {
+  if (y16) return combine(y16, ids, weights, T, topk, N, E, y, c);
+  return combine(y32, ids, weights, T, topk, N, E, y, c);
+}
+
+}  // namespace sq

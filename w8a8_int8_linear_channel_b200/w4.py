@@ -1,0 +1,306 @@
+"""4-bit weights with group scales, and mixture-of-experts layers on them.
+
+The ctypes binding of the ``sq_w4*`` and ``sq_moe_*`` entry points of
+``include/sq.h`` (argument marshalling only, like the rest of the package) and
+the two layers built from them: ``W4Linear`` beside ``SmoothQuantLinear`` for
+layers whose time is the weight's bytes, and ``W4Experts``, a routed
+feed-forward layer (up, ReLU, down) over 4-bit experts.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import _L, _check, _p, _rows, _stream, _vec
+
+MOE_MAX_EXPERTS = 512
+MOE_MAX_TOPK = 32
+GROUPS = (32, 64, 128)
+
+
+class W4Weight:
+    """A packed 4-bit weight [N, K] (or one per expert): the library's buffer and its shape."""
+
+    def __init__(self, packed: torch.Tensor, N: int, K: int, group: int, zero_point: bool,
+                 experts: Optional[int] = None):
+        need = sq_w4_packed_bytes(N, K, group, zero_point) * (1 if experts is None else experts)
+        if packed.dtype != torch.uint8 or not packed.is_contiguous() or packed.numel() != need or need == 0:
+            raise ValueError(f"packed: need a contiguous uint8 tensor of {need} bytes")
+        self.packed, self.N, self.K = packed, N, K
+        self.group, self.zero_point, self.experts = group, bool(zero_point), experts
+
+    def __getitem__(self, e: int) -> "W4Weight":
+        """Expert e's weight (a view)."""
+        if self.experts is None or not 0 <= e < self.experts:
+            raise IndexError(f"expert {e} of {self.experts}")
+        n = self.packed.numel() // self.experts
+        return W4Weight(self.packed[e * n:(e + 1) * n], self.N, self.K, self.group, self.zero_point)
+
+
+def sq_w4_packed_bytes(N: int, K: int, group: int, zero_point: bool) -> int:
+    return int(_L.sq_w4_packed_bytes(N, K, group, int(bool(zero_point))))
+
+
+def new_w4_weight(N: int, K: int, group: int = 128, zero_point: bool = False, experts: Optional[int] = None,
+                  device=None) -> W4Weight:
+    """An empty packed weight, to be filled by sq_quantize_weight_w4 or sq_w4_pack."""
+    n = sq_w4_packed_bytes(N, K, group, zero_point)
+    if n == 0 or (experts is not None and not 1 <= experts <= MOE_MAX_EXPERTS):
+        raise ValueError(f"no packed 4-bit form of N={N}, K={K}, group={group}, experts={experts} "
+                         f"(K % 16 == 0, group one of {GROUPS}, at most {MOE_MAX_EXPERTS} experts)")
+    packed = torch.empty(n * (experts or 1), dtype=torch.uint8, device=device or "cuda")
+    return W4Weight(packed, N, K, group, zero_point, experts)
+
+
+def _dense(w4: W4Weight, what: str) -> None:
+    if w4.experts is not None:
+        raise ValueError(f"{what}: a single weight is needed, this one holds {w4.experts} experts")
+
+
+def _tensor(t: torch.Tensor, dtype, shape, name: str) -> None:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} {tuple(shape)} tensor")
+
+
+def sq_quantize_weight_w4(w: torch.Tensor, w4: W4Weight, s=None, stream=None) -> W4Weight:
+    """Quantize fp16 w [N, K] ([E, N, K] for experts), folded by s [K] when given, into w4."""
+    lead = () if w4.experts is None else (w4.experts,)
+    _tensor(w, torch.float16, lead + (w4.N, w4.K), "w")
+    _vec(s, w4.K, torch.float32, "s")
+    for src, dst in ((w, w4),) if w4.experts is None else ((w[e], w4[e]) for e in range(w4.experts)):
+        _check(_L.sq_quantize_weight_w4(_p(src), w4.N, w4.K, _p(s), w4.group, int(w4.zero_point), _p(dst.packed),
+                                        _stream(stream)), "sq_quantize_weight_w4")
+    return w4
+
+
+def sq_w4_pack(codes: torch.Tensor, scales: torch.Tensor, w4: W4Weight, zeros=None, stream=None) -> W4Weight:
+    """Pack uint8 codes [N, K], fp16 scales and uint8 zeros [N, ceil(K / group)] (each with a leading
+    [E] for experts) into w4; zeros exactly when w4 has zero points."""
+    lead = () if w4.experts is None else (w4.experts,)
+    G = -(-w4.K // w4.group)
+    _tensor(codes, torch.uint8, lead + (w4.N, w4.K), "codes")
+    _tensor(scales, torch.float16, lead + (w4.N, G), "scales")
+    if (zeros is not None) != w4.zero_point:
+        raise ValueError("zeros: given exactly when the weight has zero points")
+    if zeros is not None:
+        _tensor(zeros, torch.uint8, lead + (w4.N, G), "zeros")
+    if w4.experts is None:
+        parts = [(codes, scales, zeros, w4)]
+    else:
+        parts = [(codes[e], scales[e], None if zeros is None else zeros[e], w4[e]) for e in range(w4.experts)]
+    for c, s, z, dst in parts:
+        if s.data_ptr() % 16 or (z is not None and z.data_ptr() % 16):  # an expert's slice may start off 16 bytes
+            s, z = s.clone(), None if z is None else z.clone()
+        _check(_L.sq_w4_pack(_p(c), _p(s), _p(z), w4.N, w4.K, w4.group, _p(dst.packed), _stream(stream)), "sq_w4_pack")
+    return w4
+
+
+def sq_w4_dequantize(w4: W4Weight, out: torch.Tensor, stream=None) -> torch.Tensor:
+    """out fp16 [N, K] = the values of a packed weight."""
+    _dense(w4, "sq_w4_dequantize")
+    _tensor(out, torch.float16, (w4.N, w4.K), "out")
+    _check(_L.sq_w4_dequantize(_p(w4.packed), w4.N, w4.K, w4.group, int(w4.zero_point), _p(out), _stream(stream)),
+           "sq_w4_dequantize")
+    return out
+
+
+def sq_w4a16_linear(x: torch.Tensor, w4: W4Weight, y: torch.Tensor, bias=None, relu: bool = False,
+                    stream=None) -> torch.Tensor:
+    """y fp16 [M, N] = fp16(x @ W^T + bias) with a packed 4-bit W; ReLU optional."""
+    _dense(w4, "sq_w4a16_linear")
+    M, K, ld = _rows(x, torch.float16, "x")
+    if K != w4.K:
+        raise ValueError(f"x: need [M, {w4.K}], got {tuple(x.shape)}")
+    if M == 1:
+        ld = max(ld, K)  # the stride of a single row means nothing
+    _vec(bias, w4.N, torch.float16, "bias")
+    _tensor(y, torch.float16, (M, w4.N), "y")
+    _check(_L.sq_w4a16_linear(_p(x), M, ld, _p(w4.packed), w4.N, K, w4.group, int(w4.zero_point), _p(bias),
+                              int(bool(relu)), _p(y), _stream(stream)), "sq_w4a16_linear")
+    return y
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def sq_moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, bias=None, score: str = "softmax",
+                 n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
+                 scale: float = 1.0, stream=None):
+    """The topk experts of every token (ids int32 [T, topk], largest choice first) and their weights
+    (fp32 [T, topk]) from router logits, fp32 or fp16 [T, E]."""
+    if logits.dtype not in (torch.float32, torch.float16):
+        raise ValueError("logits: fp32 or fp16")
+    if score not in _SCORES:
+        raise ValueError(f"score: one of {sorted(_SCORES)}")
+    T, E, ld = _rows(logits, logits.dtype, "logits")
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids: need [{T}, topk]")
+    topk = ids.shape[1]
+    _tensor(ids, torch.int32, (T, topk), "ids")
+    _tensor(weights, torch.float32, (T, topk), "weights")
+    _vec(bias, E, torch.float32, "bias")
+    _check(_L.sq_moe_route(_p(logits), int(logits.dtype == torch.float16), T, E, max(ld, E) if T == 1 else ld,
+                           _p(bias), _SCORES[score], n_group, topk_group, group_top, topk, int(bool(renormalize)),
+                           scale, _p(ids), _p(weights), _stream(stream)), "sq_moe_route")
+    return ids, weights
+
+
+def sq_moe_plan_workspace_bytes(pairs: int, experts: int) -> int:
+    return int(_L.sq_moe_plan_workspace_bytes(pairs, experts))
+
+
+def sq_moe_plan(ids: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor, workspace=None, stream=None):
+    """The (token, slot) pairs of ids (int32, any shape) stably sorted by expert: offsets int32
+    [E + 1], order int32 [ids.numel()].  Without a workspace one is allocated for the call."""
+    pairs, E = ids.numel(), offsets.numel() - 1
+    if ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids: need a contiguous int32 tensor")
+    _vec(offsets, E + 1, torch.int32, "offsets")
+    _vec(order, pairs, torch.int32, "order")
+    if workspace is None:
+        need = sq_moe_plan_workspace_bytes(pairs, E)
+        if need:
+            with torch.cuda.stream(stream):  # freed memory is reused in this stream's order
+                workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_L.sq_moe_plan(_p(ids), pairs, E, _p(offsets), _p(order), _p(workspace), ws_bytes, _stream(stream)),
+           "sq_moe_plan")
+    return offsets, order
+
+
+def sq_w4a16_experts(x: torch.Tensor, w4: W4Weight, offsets: torch.Tensor, order: torch.Tensor, y: torch.Tensor,
+                     pairs_per_row: int = 1, bias=None, relu: bool = False, stream=None) -> torch.Tensor:
+    """y [pairs, N] (fp16 or fp32): pair p, which the plan lists under expert e, gets
+    x[p // pairs_per_row] @ W_e^T + bias[e]; rows the plan leaves out keep their contents."""
+    if w4.experts is None:
+        raise ValueError("w4: need a weight of several experts")
+    rows, K, ld = _rows(x, torch.float16, "x")
+    if K != w4.K:
+        raise ValueError(f"x: need [rows, {w4.K}], got {tuple(x.shape)}")
+    if rows == 1:
+        ld = max(ld, K)
+    pairs = order.numel()
+    _vec(offsets, w4.experts + 1, torch.int32, "offsets")
+    _vec(order, pairs, torch.int32, "order")
+    if bias is not None:
+        _tensor(bias, torch.float16, (w4.experts, w4.N), "bias")
+    if y.dtype not in (torch.float16, torch.float32):
+        raise ValueError("y: fp16 or fp32")
+    _tensor(y, y.dtype, (pairs, w4.N), "y")
+    _check(_L.sq_w4a16_experts(_p(x), rows, ld, _p(w4.packed), w4.experts, w4.N, K, w4.group, int(w4.zero_point),
+                               _p(bias), int(bool(relu)), _p(offsets), _p(order), pairs, pairs_per_row, _p(y),
+                               int(y.dtype == torch.float32), _stream(stream)), "sq_w4a16_experts")
+    return y
+
+
+def sq_moe_combine(y_pairs: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, experts: int, y: torch.Tensor,
+                   stream=None) -> torch.Tensor:
+    """y fp16 [T, N] = the weighted sum of every token's rows of y_pairs [T * topk, N] (fp16 or fp32)."""
+    if y_pairs.dtype not in (torch.float16, torch.float32):
+        raise ValueError("y_pairs: fp16 or fp32")
+    if ids.dim() != 2:
+        raise ValueError("ids: need [T, topk]")
+    T, topk = ids.shape
+    N = y_pairs.shape[-1]
+    _tensor(ids, torch.int32, (T, topk), "ids")
+    _tensor(weights, torch.float32, (T, topk), "weights")
+    _tensor(y_pairs, y_pairs.dtype, (T * topk, N), "y_pairs")
+    _tensor(y, torch.float16, (T, N), "y")
+    _check(_L.sq_moe_combine(_p(y_pairs), int(y_pairs.dtype == torch.float32), _p(ids), _p(weights), T, topk, N,
+                             experts, _p(y), _stream(stream)), "sq_moe_combine")
+    return y
+
+
+# ------------------------------------------------------------- layer API ----
+class W4Linear:
+    """A linear layer with a packed 4-bit weight: fp16 [..., K] -> fp16 [..., N]."""
+
+    def __init__(self, w4: W4Weight, bias: Optional[torch.Tensor] = None, relu: bool = False):
+        _dense(w4, "W4Linear")
+        self.w4, self.bias, self.relu = w4, bias, relu
+
+    @classmethod
+    def from_float(cls, w: torch.Tensor, group: int = 128, zero_point: bool = False, s=None, bias=None,
+                   relu: bool = False) -> "W4Linear":
+        """Quantize an fp16 weight [N, K].  With s (fp32 [K], e.g. from sq_smooth_fold) the weight is
+        folded by it first; the layer's input is then the smoothed one, x / s."""
+        w4 = new_w4_weight(w.shape[0], w.shape[1], group, zero_point, device=w.device)
+        return cls(sq_quantize_weight_w4(w, w4, s=s), bias, relu)
+
+    def forward(self, x: torch.Tensor, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Leading dimensions are flattened into tokens; an empty batch launches nothing."""
+        N, K = self.w4.N, self.w4.K
+        if x.dim() < 1 or x.shape[-1] != K:
+            raise ValueError(f"x: need [..., {K}], got {tuple(x.shape)}")
+        lead = tuple(x.shape[:-1])
+        x2 = x if x.dim() == 2 else x.reshape(-1, K)
+        if y is None:
+            y = torch.empty(lead + (N,), dtype=torch.float16, device=x.device)
+        elif tuple(y.shape) not in (lead + (N,), (x2.shape[0], N)) or not y.is_contiguous():
+            raise ValueError(f"y: need a contiguous fp16 {lead + (N,)} tensor")
+        if x2.shape[0]:
+            sq_w4a16_linear(x2, self.w4, y.view(-1, N), self.bias, self.relu)
+        return y
+
+    __call__ = forward
+
+
+class W4Experts:
+    """A mixture-of-experts feed-forward layer on packed 4-bit weights.
+
+    up [E, F, K] and down [E, K, F]: y[t] = sum_j weight[t, j] * down_e(relu(up_e(x[t]))) over the
+    topk experts e that sq_moe_route picks for token t from its router logits."""
+
+    def __init__(self, up: W4Weight, down: W4Weight, topk: int, score: str = "softmax", router_bias=None,
+                 n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
+                 scale: float = 1.0, up_bias=None, down_bias=None):
+        if up.experts is None or up.experts != down.experts or (up.N, up.K) != (down.K, down.N):
+            raise ValueError("up / down: need [E, F, K] and [E, K, F] of the same experts")
+        self.up, self.down, self.topk = up, down, topk
+        self.score, self.router_bias = score, router_bias
+        self.n_group, self.topk_group, self.group_top = n_group, topk_group, group_top
+        self.renormalize, self.scale = renormalize, scale
+        self.up_bias, self.down_bias = up_bias, down_bias
+
+    @classmethod
+    def from_float(cls, w_up: torch.Tensor, w_down: torch.Tensor, topk: int, group: int = 128,
+                   zero_point: bool = False, **kw) -> "W4Experts":
+        """Quantize fp16 expert weights [E, F, K] and [E, K, F]; other arguments as in the constructor."""
+        packed = []
+        for w in (w_up, w_down):
+            w4 = new_w4_weight(w.shape[1], w.shape[2], group, zero_point, experts=w.shape[0], device=w.device)
+            packed.append(sq_quantize_weight_w4(w, w4))
+        return cls(packed[0], packed[1], topk, **kw)
+
+    def route(self, logits: torch.Tensor):
+        """ids int32 and weights fp32, [T, topk], of logits [T, E]."""
+        T = logits.shape[0]
+        ids = torch.empty((T, self.topk), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((T, self.topk), dtype=torch.float32, device=logits.device)
+        return sq_moe_route(logits, ids, weights, self.router_bias, self.score, self.n_group, self.topk_group,
+                            self.group_top, self.renormalize, self.scale)
+
+    def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
+        """x fp16 [..., K] and router logits [..., E] (fp32 or fp16) -> y fp16 [..., K]."""
+        E, F, K = self.up.experts, self.up.N, self.up.K
+        if x.dim() < 1 or x.shape[-1] != K or tuple(logits.shape) != tuple(x.shape[:-1]) + (E,):
+            raise ValueError(f"x / logits: need [..., {K}] and [..., {E}], got {tuple(x.shape)}, {tuple(logits.shape)}")
+        x2, l2 = x.reshape(-1, K), logits.reshape(-1, E)
+        T, P = x2.shape[0], x2.shape[0] * self.topk
+        y = torch.empty(tuple(x.shape), dtype=torch.float16, device=x.device)
+        if T == 0:
+            return y
+        ids, weights = self.route(l2)
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=x.device)
+        order = torch.empty(P, dtype=torch.int32, device=x.device)
+        sq_moe_plan(ids, offsets, order)
+        h = torch.empty((P, F), dtype=torch.float16, device=x.device)
+        sq_w4a16_experts(x2, self.up, offsets, order, h, self.topk, self.up_bias, relu=True)
+        # fp32 rows, so that the layer's output is rounded once
+        z = torch.empty((P, K), dtype=torch.float32, device=x.device)
+        sq_w4a16_experts(h, self.down, offsets, order, z, 1, self.down_bias)
+        sq_moe_combine(z, ids, weights, E, y.view(-1, K))
+        return y
+
+    __call__ = forward
