@@ -26,8 +26,8 @@ FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-fmad=
                 "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
 
 SOURCES = ["sq_api.cu", "k_rows.cu", "k_cols.cu", "k_gemm_tiled.cu", "k_gemm_pair.cu", "k_gemm_splitk.cu",
-           "sq_api_w4.cu", "k_w4_weight.cu", "k_w4_stream.cu", "k_moe.cu"]
-HEADERS = ["sq_internal.h", "sq_ptx.cuh", "sq_tmap.h", "sq_w4.h"]
+           "sq_api_w4.cu", "k_w4_weight.cu", "k_w4_stream.cu", "k_w4_gemm.cu", "k_moe.cu"]
+HEADERS = ["sq_internal.h", "sq_ptx.cuh", "sq_tmap.h", "sq_w4.h", "sq_w4.cuh"]
 
 
 def _newer(target: str, deps) -> bool:

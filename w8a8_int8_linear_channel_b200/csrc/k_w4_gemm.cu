@@ -1,0 +1,442 @@
+// k_w4_gemm.cu -- y = x W^T with a packed 4-bit W on the 5th-generation tensor
+// cores, for more tokens than k_w4_stream.cu takes.
+//
+// Swap-AB: the MMA's 128-row M slot takes 128 output channels, its N slot the
+// tokens.  The weight operand is made on the fly: a thread per channel turns
+// codes into fp16 numbers (q - z) * s in registers and stores them to tensor
+// memory, from where tcgen05.mma reads its A operand; the tokens (B) are
+// staged in shared memory.  A weight made by the library's quantizer is
+// exactly an fp16 number, so nothing is rounded before the fp32 accumulators
+// (a scale of more than 8 significant bits costs one fp16 rounding per weight).
+//
+// Why tensor memory: writing the 32 KB of a dequantized 128 x 128 tile to
+// shared memory and reading it back as the MMA's operand would take twice the
+// shared-memory bandwidth that a tile's time leaves.
+//
+// Roles: eight dequantization warps (also the epilogue), four that copy token
+// rows (cp.async: gathered rows, K tails and missing tokens need no other
+// form), one MMA issuer, one record producer.  All waits are bounded.
+#include "sq_w4.cuh"
+
+namespace sq {
+namespace {
+
+constexpr int kDequantWarps = 8;
+constexpr int kLoadWarps = 4;
+constexpr int kMmaWarp = kDequantWarps + kLoadWarps;
+constexpr int kRecordWarp = kMmaWarp + 1;
+constexpr int kThreads = (kRecordWarp + 1) * 32;
+constexpr int kMaxSlices = 8;
+constexpr int kACols = kW4K / 2;  // 32-bit TMEM columns of one 128 x 128 fp16 operand
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 operands, fp32 accumulate.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// kind::f16, fp16 A and B (both K-major), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// Thread i of the warp stores 16 registers to columns [col, col + 16) of TMEM
+// lane (lane base + i).
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Columns [col, col + 8) of the warp's lanes, complete on return.
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2_rn(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 16 bytes global -> shared, or 16 zero bytes when `bytes` is 0.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
+
+// BT tokens and RT weight tiles (128 channels each) per CTA.
+template <int BT, int RT, int G, bool ZERO>
+struct Layout {
+  static constexpr int REC = w4_record_bytes(G, ZERO);
+  static constexpr int XSTAGE = BT * kW4K * 2;             // two boxes of [BT][64 k], 128-byte swizzle
+  static constexpr int XS = BT <= 32 ? 4 : RT == 2 ? 4 : 3;  // token stages
+  static constexpr int RS = RT == 2 ? 3 : 4;               // record stages, RT records each
+  static constexpr int AS = RT == 2 ? 2 : 3;               // operand buffers in tensor memory
+  static constexpr int D_COLS = RT * BT;
+  static constexpr int A0 = D_COLS;
+  static constexpr int TMEM_COLS = D_COLS + AS * RT * kACols <= 256 ? 256 : 512;
+  static constexpr int RED_PITCH = BT + 4;
+  static constexpr int RED_BYTES = (kW4Rows + kMaxSlices) * RED_PITCH * 4;
+  // the cluster's sums reuse the token stages: by then every MMA has read them
+  static constexpr int X = 0;
+  static constexpr int R = X + (XS * XSTAGE > RED_BYTES || RT == 2 ? XS * XSTAGE : (RED_BYTES + 1023) / 1024 * 1024);
+  static constexpr int BARS = R + RS * RT * REC;
+  static constexpr int NBARS = 2 * XS + 2 * RS + 2 * AS + 1;
+  static constexpr int XROW = BARS + (NBARS * 8 + 15) / 16 * 16;  // int32 [BT]: x row of every token, -1 none
+  static constexpr int YROW = XROW + BT * 4;                      // int32 [BT]: y row
+  static constexpr int MISC = YROW + BT * 4;                      // abort, TMEM address, expert, count
+  static constexpr int BYTES = MISC + 16 + 1024;                  // alignment slack
+  static_assert(D_COLS + AS * RT * kACols <= 512, "tensor memory");
+  static_assert(BYTES <= 232448, "shared memory per CTA");
+};
+
+template <int BT, int RT, int G, bool ZERO>
+__global__ void __launch_bounds__(kThreads, RT == 2 ? 1 : 2)
+    k_w4_gemm(const W4Product p, int slices, int blocks, int KT, uint32_t* status, uint64_t budget) {
+  using L = Layout<BT, RT, G, ZERO>;
+  constexpr int NG = kW4K / G;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + L::MISC);
+  int32_t* misc = reinterpret_cast<int32_t*>(smem + L::MISC);
+  int32_t* xrow = reinterpret_cast<int32_t*>(smem + L::XROW);
+  int32_t* yrow = reinterpret_cast<int32_t*>(smem + L::YROW);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slice = blockIdx.x % slices;
+  const int block = blockIdx.x / slices % blocks;
+  const int tile = blockIdx.x / slices / blocks * RT;  // first weight tile
+  const uint32_t x_full = sbase + L::BARS, x_empty = x_full + 8 * L::XS;
+  const uint32_t r_full = x_empty + 8 * L::XS, r_empty = r_full + 8 * L::RS;
+  const uint32_t a_full = r_empty + 8 * L::RS, a_empty = a_full + 8 * L::AS;
+  const uint32_t d_full = a_empty + 8 * L::AS;
+
+  if (tid == 0) {
+    for (int s = 0; s < L::XS; ++s) mbar_init(x_full + 8 * s, kLoadWarps), mbar_init(x_empty + 8 * s, 1);
+    for (int s = 0; s < L::RS; ++s) {
+      mbar_init(r_full + 8 * s, 1);
+      mbar_init(r_empty + 8 * s, RT == 2 ? 8 : 4);
+    }
+    for (int s = 0; s < L::AS; ++s) {
+      mbar_init(a_full + 8 * s, RT == 2 ? 8 : 4);
+      mbar_init(a_empty + 8 * s, 1);
+    }
+    mbar_init(d_full, 1);
+    *abort = 0;
+    fence_barrier_init();
+  }
+  griddep_wait();
+
+  // the block's tokens, found before tensor memory is taken: a block that does
+  // not exist leaves at once
+  if (warp == 0) {
+    int expert = 0, start = 0, count = 0;
+    if (p.offsets == nullptr) {
+      const int64_t first = static_cast<int64_t>(block) * BT;
+      start = static_cast<int>(first);
+      count = static_cast<int>(p.M - first < BT ? p.M - first : BT);
+    } else {
+      expert = w4_find_block(p, block, BT, lane, &start, &count);
+    }
+    if (lane == 0) misc[2] = expert, misc[3] = count;
+    for (int i = lane; i < BT; i += 32) {
+      int32_t row = -1;
+      if (expert >= 0 && i < count) {
+        row = p.offsets ? p.order[start + i] : start + i;
+        if (row < 0 || row >= p.M) row = -1;
+      }
+      yrow[i] = row;
+      xrow[i] = row < 0 ? -1 : row / p.div;
+    }
+  }
+  __syncthreads();
+  const int expert = misc[2], count = misc[3];
+  if (expert < 0) return;  // the same for every CTA of the cluster
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(misc + 1), L::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc[1]);
+
+  const int kt0 = static_cast<int>(static_cast<int64_t>(KT) * slice / slices);
+  const int n = static_cast<int>(static_cast<int64_t>(KT) * (slice + 1) / slices) - kt0;
+  const int64_t nt = p.w.nt();
+
+  if (warp < kDequantWarps) {
+    // ---- dequantization: thread = channel; RT == 1: the two groups of four
+    // warps take even and odd K tiles, RT == 2: one weight tile each
+    const int group = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
+    for (int i = RT == 2 ? 0 : group; i < n; i += RT == 2 ? 1 : 2) {
+      const int rs = i % L::RS, as = i % L::AS;
+      if (!mbar_wait(r_full + 8 * rs, (i / L::RS) & 1, budget, status, abort)) break;
+      const int rec = L::R + (rs * RT + (RT == 2 ? group : 0)) * L::REC;
+      uint4 c[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] = lds128(sbase + rec + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+      uint32_t s2[NG], z[NG];
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        const uint32_t s = *reinterpret_cast<const uint16_t*>(smem + rec + kW4CodeBytes + (r * NG + j) * 2);
+        s2[j] = s | s << 16;
+        z[j] = ZERO ? smem[rec + kW4CodeBytes + kW4Rows * NG * 2 + r * NG + j] : 8u;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(r_empty + 8 * rs);
+      if (i >= L::AS && !mbar_wait(a_empty + 8 * as, ((i / L::AS) & 1) ^ 1, budget, status, abort)) break;
+      tc_fence_after();
+      const uint32_t col = tmem + L::A0 + (as * RT + (RT == 2 ? group : 0)) * kACols + lanes;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const int j = w / (G / 32);
+        const uint32_t lo = 0x64006400u | z[j] | z[j] << 16, hi = 0xD400D400u | z[j] << 4 | z[j] << 20;
+        const uint32_t word[4] = {w == 0 ? c[0].x : w == 1 ? c[0].y : w == 2 ? c[0].z : c[0].w,
+                                  w == 0 ? c[1].x : w == 1 ? c[1].y : w == 2 ? c[1].z : c[1].w,
+                                  w == 0 ? c[2].x : w == 1 ? c[2].y : w == 2 ? c[2].z : c[2].w,
+                                  w == 0 ? c[3].x : w == 1 ? c[3].y : w == 2 ? c[3].z : c[3].w};
+        uint32_t v[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t h[4];
+          dequant(word[q], lo, hi, h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * q + e] = hmul2(h[e], s2[j]);
+        }
+        tmem_st_x16(col + 16 * w, v);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(a_full + 8 * as);
+    }
+  } else if (warp < kMmaWarp) {
+    // ---- token rows: 16 lanes copy a row's 128 k; arrival one tile late, so
+    // two tiles are in flight per thread
+    const int lt = tid - kDequantWarps * 32;
+    const int c = lt & 15;
+    const uint32_t box = static_cast<uint32_t>(c >> 3) * (BT * 128);
+    int done = 0;
+    for (int i = 0; i < n; ++i) {
+      const int xs = i % L::XS;
+      if (i >= L::XS && !mbar_wait(x_empty + 8 * xs, ((i / L::XS) & 1) ^ 1, budget, status, abort)) break;
+      const uint32_t stage = sbase + L::X + xs * L::XSTAGE + box;
+      const int64_t k = static_cast<int64_t>(kt0 + i) * kW4K + 8 * c;
+#pragma unroll
+      for (int j = 0; j < BT / 8; ++j) {
+        const int row = (lt >> 4) + 8 * j;
+        const int32_t xr = xrow[row];
+        const bool live = xr >= 0 && k < p.w.K;
+        cp_async16(stage + row * 128 + (((c & 7) ^ (row & 7)) << 4), live ? p.x + xr * p.ldx + k : p.x, live ? 16 : 0);
+      }
+      cp_async_commit();
+      if (i > 0) {
+        cp_async_wait<1>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x_full + 8 * (done % L::XS));
+        ++done;
+      }
+    }
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (done < n && lane == 0) mbar_arrive(x_full + 8 * (done % L::XS));
+  } else if (warp == kMmaWarp) {
+    // ---- MMA issue
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16(kW4Rows, BT);
+      for (int i = 0; i < n; ++i) {
+        const int xs = i % L::XS, as = i % L::AS;
+        if (!mbar_wait(a_full + 8 * as, (i / L::AS) & 1, budget, status, abort)) break;
+        if (!mbar_wait(x_full + 8 * xs, (i / L::XS) & 1, budget, status, abort)) break;
+        tc_fence_after();
+        const uint64_t b0 = sdesc_k_sw128(sbase + L::X + xs * L::XSTAGE);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t b = b0 + (((j >> 2) * BT * 128 + (j & 3) * 32) >> 4);
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+            mma_f16_ts(tmem + t * BT, tmem + L::A0 + (as * RT + t) * kACols + 8 * j, b, idesc, i > 0 || j > 0);
+        }
+        mma_commit(a_empty + 8 * as);
+        mma_commit(x_empty + 8 * xs);
+      }
+      mma_commit(d_full);  // also after a wait that ran out: nothing in flight is left behind
+    }
+  } else if (lane == 0) {
+    // ---- record producer
+    int issued = 0;
+    for (int i = 0; i < n; ++i) {
+      const int rs = i % L::RS;
+      if (i >= L::RS && !mbar_wait(r_empty + 8 * rs, ((i / L::RS) & 1) ^ 1, budget, status, abort)) break;
+      // the last weight tile may stand alone: its place is taken by itself
+      // again, and nothing of the copy is written out
+      mbar_arrive_expect_tx(r_full + 8 * rs, RT * L::REC);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const int64_t wt = tile + t < nt ? tile + t : nt - 1;
+        bulk_load(sbase + L::R + (rs * RT + t) * L::REC,
+                  p.w.data + ((static_cast<int64_t>(expert) * nt + wt) * KT + kt0 + i) * L::REC, L::REC, r_full + 8 * rs);
+      }
+      issued = i + 1;
+    }
+    // records in flight land before the CTA can leave (at once unless a wait ran out)
+    for (int i = max(0, issued - L::RS); i < issued; ++i)
+      mbar_drain(r_full + 8 * (i % L::RS), (i / L::RS) & 1, budget);
+  }
+  __syncwarp();
+
+  // ---- epilogue
+  mbar_drain(d_full, 0, budget);
+  tc_fence_after();
+  griddep_launch_dependents();
+  if (slices > 1) cluster_sync_all();  // the token stages of every CTA are free
+  if (warp < kDequantWarps) {
+    const int group = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const int t = RT == 2 ? group : 0;
+    const int c0 = RT == 2 ? 0 : group * (BT / 2), c1 = RT == 2 ? BT : c0 + BT / 2;
+    const int64_t ch = static_cast<int64_t>(tile + t) * kW4Rows + r;
+    float bias = 0.0f;
+    if (p.bias && ch < p.w.N) bias = __half2float(p.bias[static_cast<int64_t>(expert) * p.w.N + ch]);
+    const int share = (kW4Rows + slices - 1) / slices;
+    constexpr int STEP = 8;
+    for (int col = c0; col < c1; col += STEP) {
+      if (col >= count) break;  // no token of this block lies there
+      uint32_t v[8];
+      tmem_ld_x8(tmem + t * BT + col + lanes, v);
+      if (slices > 1) {
+        const int owner = r / share;
+        const uint32_t at =
+            mapa_shared(sbase + ((slice * share + r - owner * share) * L::RED_PITCH + col) * 4, owner);
+#pragma unroll
+        for (int j = 0; j < STEP; j += 4) {
+          st_cluster_v4(at + j * 4, __uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
+                        __uint_as_float(v[j + 3]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < STEP; ++j) {
+          const int32_t row = yrow[col + j];
+          if (row < 0 || ch >= p.w.N) continue;
+          float f = __uint_as_float(v[j]);
+          if (p.bias) f = __fadd_rn(f, bias);
+          if (p.relu) f = f > 0.0f ? f : 0.0f;
+          const int64_t o = static_cast<int64_t>(row) * p.w.N + ch;
+          if (p.y)
+            p.y[o] = __float2half_rn(f);
+          else
+            p.y32[o] = f;
+        }
+      }
+    }
+  }
+  if (slices > 1) {
+    cluster_sync_all();  // releases the pushes; nothing of this CTA is touched from outside after it
+    const int share = (kW4Rows + slices - 1) / slices;
+    const float* red = reinterpret_cast<const float*>(smem);
+    const int64_t n0 = static_cast<int64_t>(tile) * kW4Rows + slice * share;
+    const int64_t left = min(p.w.N - n0, static_cast<int64_t>(kW4Rows - slice * share));
+    const int width = static_cast<int>(left < share ? left : share);
+    for (int i = tid; i < width * count; i += kThreads) {
+      const int tk = i / width, q = i - tk * width;
+      const int32_t row = yrow[tk];
+      if (row < 0) continue;
+      float f = 0.0f;
+#pragma unroll 4
+      for (int s = 0; s < slices; ++s) f = __fadd_rn(f, red[(s * share + q) * L::RED_PITCH + tk]);
+      if (p.bias) f = __fadd_rn(f, __half2float(p.bias[static_cast<int64_t>(expert) * p.w.N + n0 + q]));
+      if (p.relu) f = f > 0.0f ? f : 0.0f;
+      const int64_t o = static_cast<int64_t>(row) * p.w.N + n0 + q;
+      if (p.y)
+        p.y[o] = __float2half_rn(f);
+      else
+        p.y32[o] = f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, L::TMEM_COLS);
+}
+
+template <int BT, int RT, int G, bool ZERO>
+cudaError_t launch(const W4Product& p, const Ctx& c) {
+  using L = Layout<BT, RT, G, ZERO>;
+  auto kernel = k_w4_gemm<BT, RT, G, ZERO>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (p.w.nt() + RT - 1) / RT, kt = p.w.kt();
+  const int64_t blocks = w4_blocks(p, BT);
+  const int slices = RT == 2 ? 1 : w4_slices(tiles * blocks, kt, static_cast<int64_t>(c.num_sms) * 2, 6);
+  if (tiles * blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * blocks * slices));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::BYTES;
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = slices;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, slices, static_cast<int>(blocks), static_cast<int>(kt), c.status,
+                            c.budget_ns);
+}
+
+template <int BT, int RT>
+cudaError_t launch_g(const W4Product& p, const Ctx& c) {
+  if (p.w.zero) {
+    if (p.w.group == 32) return launch<BT, RT, 32, true>(p, c);
+    if (p.w.group == 64) return launch<BT, RT, 64, true>(p, c);
+    return launch<BT, RT, 128, true>(p, c);
+  }
+  if (p.w.group == 32) return launch<BT, RT, 32, false>(p, c);
+  if (p.w.group == 64) return launch<BT, RT, 64, false>(p, c);
+  return launch<BT, RT, 128, false>(p, c);
+}
+
+}  // namespace
+
+cudaError_t launch_w4_gemm(const W4Product& p, const Ctx& c, int64_t tokens) {
+  if (tokens <= 16) return launch_g<16, 1>(p, c);
+  if (tokens <= 32) return launch_g<32, 1>(p, c);
+  if (tokens <= 64) return launch_g<64, 1>(p, c);
+  return launch_g<128, 2>(p, c);
+}
+
+}  // namespace sq

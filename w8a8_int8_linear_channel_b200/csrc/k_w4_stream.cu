@@ -8,33 +8,29 @@
 // 8-column one (fp32 accumulators); a group's sum is multiplied by its scale
 // once, in fp32, so no weight is ever rounded.
 //
-// A CTA owns one 128-channel tile and a slice of K; the cluster's CTAs own
-// the slices of the same tile and add their sums through distributed shared
-// memory at the end (in slice order: no atomics, no workspace, the same bits
-// on every run).  One warp streams records and token rows into a ring of
-// stages with bulk copies; eight warps consume them, 16 channels each.
-#include "sq_ptx.cuh"
-#include "sq_w4.h"
+// A CTA owns one 128-channel tile and a slice of K; the CTAs of a cluster own
+// the slices of one tile.  One warp streams records and token rows into a ring
+// of stages with bulk copies; eight warps consume them: four groups of 32
+// channels, times two that take the even and the odd K tiles.  At the end
+// every warp pushes its sums to the CTA of the cluster that finishes those
+// channels (distributed shared memory), which adds them in a fixed order: no
+// atomics, no workspace, the same bits on every run.
+#include "sq_w4.cuh"
 
 namespace sq {
 namespace {
 
-constexpr int kConsumers = 8;
+constexpr int kRowGroups = 4;   // warps along the channels, 32 each
+constexpr int kKGroups = 2;     // warps along K: even and odd tiles
+constexpr int kConsumers = kRowGroups * kKGroups;
 constexpr int kThreads = (kConsumers + 1) * 32;
+constexpr int kMaxSlices = 8;   // portable cluster size
 // Bytes between two tokens' 128 k in a stage: 256 + 64, so the eight lanes of
 // a 16-byte read phase (two tokens x four chunks) hit different banks.
 constexpr int kTokenPitch = 320;
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_v2(uint32_t addr, float a, float b) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -46,67 +42,103 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t h2(float v) {
-  const __half2 h = __float2half2_rn(v);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
-                            *reinterpret_cast<const __half2*>(&c));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-__device__ __forceinline__ uint32_t mask_or(uint32_t v, uint32_t mask) {
-  uint32_t r;  // (v & mask) | 0x64006400
-  asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(r) : "r"(v), "r"(mask));
-  return r;
-}
-
-// The eight codes of a word minus their zero point as four fp16 pairs.  The
-// bits 0x6400 | q are the number 1024 + q, 0x6400 | 16 q is 1024 + 16 q: one
-// subtraction (bias_lo = 1024 + z) or one fused multiply-add by 1/16
-// (bias_hi = -(64 + z)) gives q - z, both exact.
-__device__ __forceinline__ void dequant(uint32_t word, uint32_t bias_lo, uint32_t bias_hi, uint32_t (&h)[4]) {
-  const uint32_t up = word >> 8;
-  constexpr uint32_t kSixteenth = 0x2C002C00u;  // 1/16, twice
-  h[0] = hsub2(mask_or(word, 0x000F000Fu), bias_lo);
-  h[1] = hfma2(mask_or(word, 0x00F000F0u), kSixteenth, bias_hi);
-  h[2] = hsub2(mask_or(up, 0x000F000Fu), bias_lo);
-  h[3] = hfma2(mask_or(up, 0x00F000F0u), kSixteenth, bias_hi);
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-
 template <int NB, int G, bool ZERO>
 struct Layout {
   static constexpr int BT = 8 * NB;
   static constexpr int REC = w4_record_bytes(G, ZERO);
   static constexpr int X = REC;
   static constexpr int STAGE = REC + BT * kTokenPitch;
-  static constexpr int STAGES = NB == 1 ? 6 : NB == 2 ? 5 : 4;
-  static constexpr int RED = STAGES * STAGE;               // fp32 [BT][kRedPitch]
-  static constexpr int kRedPitch = kW4Rows + 4;
-  static constexpr int BARS = RED + BT * kRedPitch * 4;    // full[STAGES], empty[STAGES]
+  static constexpr int STAGES = NB == 1 ? 6 : 4;  // even: a K group keeps to its half of the stages
+  // sums of every slice and K group for the channels this CTA finishes:
+  // fp32 [slices * kKGroups][channels per CTA][BT]
+  static constexpr int RED = STAGES * STAGE;
+  static constexpr int RED_ROWS = kKGroups * (kW4Rows + kMaxSlices);
+  static constexpr int BARS = RED + RED_ROWS * BT * 4;     // full[STAGES], empty[STAGES]
   static constexpr int ROWS = BARS + 16 * STAGES;          // int32 pair index of every token of the block
-  static constexpr int MISC = ROWS + BT * 4;               // abort flag, block's first pair, pair count, expert
+  static constexpr int MISC = ROWS + BT * 4;               // abort flag, expert, token count
   static constexpr int BYTES = MISC + 16;
 };
+
+// One K tile of 32 channels x BT tokens.  Channels r0 + 16 m + (0, 8); klen is
+// how many of the tile's k exist (past them a stage holds stale token bytes).
+template <int NB, int G, bool ZERO, bool TAIL>
+__device__ __forceinline__ void consume(uint32_t stage, const uint8_t* rec, int r0, int lane, int klen,
+                                        float (&acc)[2][NB][4]) {
+  using L = Layout<NB, G, ZERO>;
+  constexpr int NG = kW4K / G;
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t w[2][2][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    // (r >> 1) & 3 is the same for r0, r0 + 8, r0 + 16, r0 + 24
+    const uint32_t off = stage + (r0 + 16 * m) * 64 + ((t ^ ((r0 >> 1) & 3)) << 4);
+    const uint4 c0 = lds128(off), c1 = lds128(off + 8 * 64);
+    w[m][0][0] = c0.x, w[m][0][1] = c0.y, w[m][0][2] = c0.z, w[m][0][3] = c0.w;
+    w[m][1][0] = c1.x, w[m][1][1] = c1.y, w[m][1][2] = c1.z, w[m][1][3] = c1.w;
+  }
+  const __half* sc = reinterpret_cast<const __half*>(rec + kW4CodeBytes) + r0 * NG;
+  const uint8_t* zp = rec + kW4CodeBytes + kW4Rows * NG * 2 + r0 * NG;
+  const uint32_t xa = stage + L::X + g * kTokenPitch + 16 * t;
+#pragma unroll
+  for (int gi = 0; gi < NG; ++gi) {
+    float part[2][NB][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[m][b][j] = 0.0f;
+    uint32_t lo[2][2], hi[2][2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        lo[m][h] = 0x64086408u, hi[m][h] = 0xD480D480u;  // z = 8: 1032, -72
+        if (ZERO) {
+          // 0x6400 | z is 1024 + z; -(64 + z) is 0xD400 | 16 z
+          const uint32_t z = zp[(16 * m + 8 * h) * NG + gi];
+          lo[m][h] = 0x64006400u | z | z << 16;
+          hi[m][h] = 0xD400D400u | z << 4 | z << 20;
+        }
+      }
+#pragma unroll
+    for (int q = gi * (G / 32); q < (gi + 1) * (G / 32); ++q) {
+      uint4 x[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        x[b] = make_uint4(0, 0, 0, 0);
+        if (!TAIL || 32 * q + 8 * t < klen) x[b] = lds128(xa + 8 * b * kTokenPitch + 64 * q);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        uint32_t a0[4], a1[4];
+        dequant(w[m][0][q], lo[m][0], hi[m][0], a0);
+        dequant(w[m][1][q], lo[m][1], hi[m][1], a1);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          mma_f16(part[m][b], a0[0], a1[0], a0[1], a1[1], x[b].x, x[b].y);
+          mma_f16(part[m][b], a0[2], a1[2], a0[3], a1[3], x[b].z, x[b].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const float s0 = __half2float(sc[16 * m * NG + gi]), s1 = __half2float(sc[(16 * m + 8) * NG + gi]);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        acc[m][b][0] = __fmaf_rn(s0, part[m][b][0], acc[m][b][0]);
+        acc[m][b][1] = __fmaf_rn(s0, part[m][b][1], acc[m][b][1]);
+        acc[m][b][2] = __fmaf_rn(s1, part[m][b][2], acc[m][b][2]);
+        acc[m][b][3] = __fmaf_rn(s1, part[m][b][3], acc[m][b][3]);
+      }
+    }
+  }
+}
 
 template <int NB, int G, bool ZERO>
 __global__ void __launch_bounds__(kThreads)
     k_w4_stream(const W4Product p, int slices, int blocks, int KT, uint32_t* status, uint64_t budget) {
   using L = Layout<NB, G, ZERO>;
-  constexpr int NG = kW4K / G;
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + L::MISC);
@@ -123,7 +155,7 @@ __global__ void __launch_bounds__(kThreads)
   if (tid == 0) {
     for (int s = 0; s < L::STAGES; ++s) {
       mbar_init(full + 8 * s, 1);
-      mbar_init(empty + 8 * s, kConsumers);
+      mbar_init(empty + 8 * s, kRowGroups);
     }
     *abort = 0;
     fence_barrier_init();
@@ -135,164 +167,129 @@ __global__ void __launch_bounds__(kThreads)
   if (p.offsets == nullptr) {
     const int64_t first = static_cast<int64_t>(block) * L::BT;
     count = static_cast<int>(p.M - first < L::BT ? p.M - first : L::BT);
-    if (tid < L::BT) rows[tid] = static_cast<int32_t>(first + tid);
+    if (tid < L::BT) rows[tid] = tid < count ? static_cast<int32_t>(first + tid) : -1;
+    __syncthreads();
   } else {
-    // block number `block` of the blocks of all experts in order: a scan of
-    // ceil(n_e / BT) over the experts
     if (warp == 0) {
-      int before = 0, found = -1, first = 0, n = 0;
-      for (int e0 = 0; e0 < p.E && found < 0; e0 += 32) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
-        if (e < p.E) {
-          lo = p.offsets[e];
-          hi = p.offsets[e + 1];
-          // offsets that no plan wrote must not lead out of the order array
-          lo = max(lo, 0);
-          hi = static_cast<int>(min(static_cast<int64_t>(hi), p.M));
-        }
-        const int mine = hi > lo ? (hi - lo + L::BT - 1) / L::BT : 0;
-        int inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int up = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += up;
-        }
-        const int rel = block - before;
-        const unsigned hit = __ballot_sync(0xffffffffu, rel >= inc - mine && rel < inc);
-        if (hit) {
-          const int src = __ffs(hit) - 1;
-          const int skip = (rel - __shfl_sync(0xffffffffu, inc - mine, src)) * L::BT;
-          first = __shfl_sync(0xffffffffu, lo, src) + skip;
-          n = min(__shfl_sync(0xffffffffu, hi, src) - first, L::BT);
-          found = e0 + src;
-        }
-        before += __shfl_sync(0xffffffffu, inc, 31);
-      }
+      int start = 0;
+      expert = w4_find_block(p, block, L::BT, lane, &start, &count);
       if (lane == 0) {
-        misc[1] = found;
-        misc[2] = n;
+        misc[1] = expert;
+        misc[2] = count;
       }
-      if (found >= 0) {
-        for (int i = lane; i < n; i += 32) {
-          const int32_t pair = p.order[first + i];
+      if (expert >= 0)
+        for (int i = lane; i < L::BT; i += 32) {
+          const int32_t pair = i < count ? p.order[start + i] : -1;
           rows[i] = pair >= 0 && pair < p.M ? pair : -1;
         }
-      }
     }
     __syncthreads();
     expert = misc[1];
     count = misc[2];
     if (expert < 0) return;  // the same for every CTA of the cluster
   }
-  __syncthreads();
 
   const int kt0 = static_cast<int>(static_cast<int64_t>(KT) * slice / slices);
-  const int kt1 = static_cast<int>(static_cast<int64_t>(KT) * (slice + 1) / slices);
-  const int64_t nt = p.w.nt();
-  const int64_t K = p.w.K;
-
-  float acc[NB][4];
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[b][i] = 0.0f;
+  const int n = static_cast<int>(static_cast<int64_t>(KT) * (slice + 1) / slices) - kt0;
+  const int tail = static_cast<int>(p.w.K & (kW4K - 1));  // k of the last tile when it is short
+  const int share = (kW4Rows + slices - 1) / slices;       // channels each CTA of the cluster finishes
 
   int issued = 0;  // stages the producer filled
   if (warp == kConsumers) {
     // ---- producer: one record and the block's token rows per stage
-    const uint8_t* recs = p.w.data + ((static_cast<int64_t>(expert) * nt + tile) * KT) * L::REC;
+    const uint8_t* rec = p.w.data + ((static_cast<int64_t>(expert) * p.w.nt() + tile) * KT + kt0) * L::REC;
     const __half* xrow = nullptr;
-    if (lane < count && rows[lane] >= 0) xrow = p.x + static_cast<int64_t>(rows[lane] / p.div) * p.ldx;
+    if (lane < count && rows[lane] >= 0)
+      xrow = p.x + static_cast<int64_t>(rows[lane] / p.div) * p.ldx + static_cast<int64_t>(kt0) * kW4K;
     const int live = __popc(__ballot_sync(0xffffffffu, xrow != nullptr));
-    for (int kt = kt0; kt < kt1; ++kt) {
-      const int i = kt - kt0, s = i % L::STAGES;
-      if (i >= L::STAGES && !mbar_wait(empty + 8 * s, ((i / L::STAGES) & 1) ^ 1, budget, status, abort)) break;
-      const uint32_t stage = sbase + s * L::STAGE;
-      const uint32_t xbytes = static_cast<uint32_t>(min(static_cast<int64_t>(kW4K), K - static_cast<int64_t>(kt) * kW4K)) * 2;
+    uint32_t stage = sbase, bar = full, phase = 1;
+    for (int i = 0; i < n; ++i) {
+      if (i >= L::STAGES && !mbar_wait(bar + 8 * L::STAGES, phase, budget, status, abort)) break;
+      const uint32_t xbytes = tail && kt0 + i == KT - 1 ? 2 * tail : 2 * kW4K;
       if (lane == 0) {
-        mbar_arrive_expect_tx(full + 8 * s, L::REC + live * xbytes);
-        bulk_load(stage, recs + static_cast<int64_t>(kt) * L::REC, L::REC, full + 8 * s);
+        mbar_arrive_expect_tx(bar, L::REC + live * xbytes);
+        bulk_load(stage, rec, L::REC, bar);
       }
       __syncwarp();
-      if (xrow) bulk_load(stage + L::X + lane * kTokenPitch, xrow + static_cast<int64_t>(kt) * kW4K, xbytes, full + 8 * s);
+      if (xrow) {
+        bulk_load(stage + L::X + lane * kTokenPitch, xrow, xbytes, bar);
+        xrow += kW4K;
+      }
+      rec += L::REC;
       issued = i + 1;
+      stage += L::STAGE;
+      bar += 8;
+      if (bar == full + 8 * L::STAGES) {
+        stage = sbase;
+        bar = full;
+        phase ^= 1;
+      }
+    }
+    if (slices > 1) {
+      cluster_arrive();  // every CTA of the cluster runs: its shared memory may be written
+      cluster_wait();
     }
   } else {
-    // ---- consumers: channels 16 * warp + (g, g + 8)
+    // ---- consumers
     const int g = lane >> 2, t = lane & 3;
-    const int r0 = warp * 16 + g;
-    const uint32_t off0 = r0 * 64 + ((t ^ ((r0 >> 1) & 3)) << 4);
-    const uint32_t off1 = off0 + 8 * 64;  // (r0 + 8) >> 1 has the same low two bits
-    bool tok[NB];
+    const int kg = warp / kRowGroups;
+    const int r0 = (warp % kRowGroups) * 32 + g;
+    if (slices > 1) cluster_arrive();
+    // token slots without a row are zero in every stage, once
+    for (int tk = warp; tk < L::BT; tk += kConsumers)
+      if (rows[tk] < 0)
+        for (int i = lane; i < L::STAGES * 16; i += 32)
+          *reinterpret_cast<uint4*>(smem + (i >> 4) * L::STAGE + L::X + tk * kTokenPitch + (i & 15) * 16) =
+              make_uint4(0, 0, 0, 0);
+    named_bar_sync(1, kConsumers * 32);
+    float acc[2][NB][4];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) tok[b] = 8 * b + g < count && rows[8 * b + g] >= 0;
-    for (int kt = kt0; kt < kt1; ++kt) {
-      const int i = kt - kt0, s = i % L::STAGES;
-      if (!mbar_wait(full + 8 * s, (i / L::STAGES) & 1, budget, status, abort)) break;
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.0f;
+    uint32_t s = kg, phase = 0;
+    for (int i = kg; i < n; i += kKGroups) {
+      if (!mbar_wait(full + 8 * s, phase, budget, status, abort)) break;
       const uint32_t stage = sbase + s * L::STAGE;
-      const uint4 c0 = lds128(stage + off0), c1 = lds128(stage + off1);
-      const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
-      const uint8_t* rec = smem + s * L::STAGE;
-      const __half* sc = reinterpret_cast<const __half*>(rec + kW4CodeBytes);
-      const uint8_t* zp = rec + kW4CodeBytes + kW4Rows * NG * 2;
-      // k of this tile that exist: past them the stage's token bytes are stale
-      const int klen = static_cast<int>(min(static_cast<int64_t>(kW4K), K - static_cast<int64_t>(kt) * kW4K));
-#pragma unroll
-      for (int gi = 0; gi < NG; ++gi) {
-        const float s0 = __half2float(sc[r0 * NG + gi]), s1 = __half2float(sc[(r0 + 8) * NG + gi]);
-        uint32_t lo0 = 0x64086408u, hi0 = 0xD480D480u, lo1 = lo0, hi1 = hi0;  // z = 8: 1032, -72
-        if (ZERO) {
-          const float z0 = zp[r0 * NG + gi], z1 = zp[(r0 + 8) * NG + gi];
-          lo0 = h2(1024.0f + z0), hi0 = h2(-64.0f - z0);
-          lo1 = h2(1024.0f + z1), hi1 = h2(-64.0f - z1);
-        }
-        float part[NB][4];
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) part[b][j] = 0.0f;
-#pragma unroll
-        for (int w = gi * (G / 32); w < (gi + 1) * (G / 32); ++w) {
-          uint32_t a0[4], a1[4];
-          dequant(w0[w], lo0, hi0, a0);
-          dequant(w1[w], lo1, hi1, a1);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (tok[b] && 32 * w + 8 * t < klen)
-              x = lds128(stage + L::X + (8 * b + g) * kTokenPitch + 64 * w + 16 * t);
-            mma_f16(part[b], a0[0], a1[0], a0[1], a1[1], x.x, x.y);
-            mma_f16(part[b], a0[2], a1[2], a0[3], a1[3], x.z, x.w);
-          }
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          acc[b][0] = __fmaf_rn(s0, part[b][0], acc[b][0]);
-          acc[b][1] = __fmaf_rn(s0, part[b][1], acc[b][1]);
-          acc[b][2] = __fmaf_rn(s1, part[b][2], acc[b][2]);
-          acc[b][3] = __fmaf_rn(s1, part[b][3], acc[b][3]);
-        }
-      }
+      if (tail && kt0 + i == KT - 1)
+        consume<NB, G, ZERO, true>(stage, smem + s * L::STAGE, r0, lane, tail, acc);
+      else
+        consume<NB, G, ZERO, false>(stage, smem + s * L::STAGE, r0, lane, kW4K, acc);
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + 8 * s);
+      s += kKGroups;
+      if (s >= L::STAGES) {
+        s -= L::STAGES;
+        phase ^= 1;
+      }
     }
-    float* red = reinterpret_cast<float*>(smem + L::RED);
+    // push the sums to the CTAs that finish these channels
+    if (slices > 1) cluster_wait();
+    const uint32_t src = (slice * kKGroups + kg) * share;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float* q = red + (8 * b + 2 * t) * L::kRedPitch + r0;
-      q[0] = acc[b][0];
-      q[L::kRedPitch] = acc[b][1];
-      q[8] = acc[b][2];
-      q[L::kRedPitch + 8] = acc[b][3];
-    }
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = r0 + 16 * m + 8 * h;
+        const int owner = r / share;
+        uint32_t at = sbase + L::RED + ((src + r - owner * share) * L::BT + 2 * t) * 4;
+        if (slices > 1) at = mapa_shared(at, owner);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          if (slices > 1)
+            st_cluster_v2(at + 32 * b, acc[m][b][2 * h], acc[m][b][2 * h + 1]);
+          else
+            *reinterpret_cast<float2*>(smem + (at - sbase) + 32 * b) = make_float2(acc[m][b][2 * h], acc[m][b][2 * h + 1]);
+        }
+      }
   }
   griddep_launch_dependents();
   if (slices > 1)
-    cluster_sync_all();
+    cluster_sync_all();  // releases the pushes; nothing of this CTA is touched from outside after it
   else
     __syncthreads();
-
   if (*abort && warp == kConsumers) {
     // a wait ran out: let the copies in flight land before the CTA leaves
     for (int i = max(0, issued - L::STAGES); i < issued; ++i)
@@ -300,29 +297,24 @@ __global__ void __launch_bounds__(kThreads)
   }
 
   // Each CTA of the cluster finishes its share of the tile's channels.
-  const int n0 = kW4Rows * slice / slices, n1 = kW4Rows * (slice + 1) / slices;
-  const int width = n1 - n0;
-  const uint32_t red = sbase + L::RED;
+  const float* red = reinterpret_cast<const float*>(smem + L::RED);
+  const int64_t n0 = static_cast<int64_t>(tile) * kW4Rows + slice * share;
+  const int64_t left = min(p.w.N - n0, static_cast<int64_t>(kW4Rows - slice * share));
+  const int width = static_cast<int>(left < share ? left : share);
   for (int i = tid; i < width * count; i += kThreads) {
-    const int tk = i / width, r = n0 + (i - tk * width);
-    const int64_t n = static_cast<int64_t>(tile) * kW4Rows + r;
-    if (n >= p.w.N || rows[tk] < 0) continue;
+    const int tk = i / width, r = i - tk * width;
+    if (rows[tk] < 0) continue;
     float v = 0.0f;
-    const uint32_t off = red + (tk * L::kRedPitch + r) * 4;
-    if (slices > 1) {
-      for (int c = 0; c < slices; ++c) v = __fadd_rn(v, ld_cluster_f32(mapa_shared(off, c)));
-    } else {
-      v = *reinterpret_cast<const float*>(smem + (off - sbase));
-    }
-    if (p.bias) v = __fadd_rn(v, __half2float(p.bias[static_cast<int64_t>(expert) * p.w.N + n]));
+#pragma unroll 4
+    for (int c = 0; c < slices * kKGroups; ++c) v = __fadd_rn(v, red[(c * share + r) * L::BT + tk]);
+    if (p.bias) v = __fadd_rn(v, __half2float(p.bias[static_cast<int64_t>(expert) * p.w.N + n0 + r]));
     if (p.relu) v = v > 0.0f ? v : 0.0f;
-    const int64_t o = static_cast<int64_t>(rows[tk]) * p.w.N + n;
+    const int64_t o = static_cast<int64_t>(rows[tk]) * p.w.N + n0 + r;
     if (p.y)
       p.y[o] = __float2half_rn(v);
     else
       p.y32[o] = v;
   }
-  if (slices > 1) cluster_sync_all();  // the others may still read this CTA's sums
 }
 
 template <int NB, int G, bool ZERO>
@@ -332,13 +324,10 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return e;
   const int64_t nt = p.w.nt(), kt = p.w.kt();
-  // Blocks of BT tokens: exactly, or for experts the most that any routing
-  // of p.M pairs can need (CTAs of blocks that do not exist leave at once).
-  int64_t blocks = (p.M + L::BT - 1) / L::BT;
-  if (p.offsets) blocks = p.M < blocks + p.E ? p.M : blocks + p.E;
-  // K is split until about two CTAs per SM exist, four tiles each at least.
-  int slices = 1;
-  while (slices < 8 && nt * blocks * slices < 2 * c.num_sms && kt / (slices + 1) >= 4) ++slices;
+  const int64_t blocks = w4_blocks(p, L::BT);
+  int per_sm = 0;
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, L::BYTES)) != cudaSuccess) return e;
+  const int slices = w4_slices(nt * blocks, kt, static_cast<int64_t>(c.num_sms) * (per_sm > 0 ? per_sm : 1), 6);
   cudaLaunchConfig_t cfg = {};
   if (nt * blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3(static_cast<unsigned>(nt * blocks * slices));
@@ -371,11 +360,34 @@ cudaError_t launch_g(const W4Product& p, const Ctx& c) {
 
 }  // namespace
 
+cudaError_t launch_w4_stream(const W4Product& p, const Ctx& c, int64_t tokens) {
+  if (tokens <= 8) return launch_g<1>(p, c);
+  return launch_g<2>(p, c);
+}
+
+int64_t w4_blocks(const W4Product& p, int bt) {
+  const int64_t blocks = (p.M + bt - 1) / bt;
+  if (!p.offsets) return blocks;
+  return p.M < blocks + p.E ? p.M : blocks + p.E;
+}
+
+int w4_slices(int64_t units, int64_t kt, int64_t slots, int start_tiles) {
+  int slices = 1;
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= kMaxSlices && (s == 1 || kt / s >= 4); ++s) {
+    const int64_t cost = ((units * s + slots - 1) / slots) * ((kt + s - 1) / s + start_tiles);
+    if (cost < best) {
+      best = cost;
+      slices = s;
+    }
+  }
+  return slices;
+}
+
 cudaError_t launch_w4_product(const W4Product& p, const Ctx& c) {
-  const int64_t per = p.offsets ? (p.M + p.E - 1) / p.E : p.M;
-  if (per <= 8) return launch_g<1>(p, c);
-  if (per <= 16) return launch_g<2>(p, c);
-  return launch_g<4>(p, c);
+  // the tokens that share a weight tile: for experts the average
+  const int64_t tokens = p.offsets ? (p.M + p.E - 1) / p.E : p.M;
+  return tokens <= 8 ? launch_w4_stream(p, c, tokens) : launch_w4_gemm(p, c, tokens);
 }
 
 }  // namespace sq

@@ -1,0 +1,90 @@
+// sq_w4.cuh -- device code shared by the 4-bit weight kernels.
+#pragma once
+
+#include "sq_ptx.cuh"
+#include "sq_w4.h"
+
+namespace sq {
+
+// Untiled bulk copy global -> shared (16-byte aligned, a multiple of 16
+// bytes), completion counted on `bar` in bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
+                            *reinterpret_cast<const __half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t mask_or(uint32_t v, uint32_t mask) {
+  uint32_t r;  // (v & mask) | 0x64006400
+  asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(r) : "r"(v), "r"(mask));
+  return r;
+}
+
+// The eight codes of a word minus their zero point as four fp16 pairs.  The
+// bits 0x6400 | q are the number 1024 + q, 0x6400 | 16 q is 1024 + 16 q: one
+// subtraction (bias_lo = 1024 + z) or one fused multiply-add by 1/16
+// (bias_hi = -(64 + z)) gives q - z, both exact.
+__device__ __forceinline__ void dequant(uint32_t word, uint32_t bias_lo, uint32_t bias_hi, uint32_t (&h)[4]) {
+  const uint32_t up = word >> 8;
+  constexpr uint32_t kSixteenth = 0x2C002C00u;  // 1/16, twice
+  h[0] = hsub2(mask_or(word, 0x000F000Fu), bias_lo);
+  h[1] = hfma2(mask_or(word, 0x00F000F0u), kSixteenth, bias_hi);
+  h[2] = hsub2(mask_or(up, 0x000F000Fu), bias_lo);
+  h[3] = hfma2(mask_or(up, 0x00F000F0u), kSixteenth, bias_hi);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// Block number `block` of the token blocks of all experts in order (ceil(n_e /
+// bt) blocks of expert e): its expert (-1: there is no such block), first plan
+// entry and token count.  Warp-collective; every lane gets the answer.
+__device__ __forceinline__ int w4_find_block(const W4Product& p, int block, int bt, int lane, int* start, int* count) {
+  int before = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 32) {
+    int lo = 0, hi = 0;
+    if (e0 + lane < p.E) {
+      // offsets that no plan wrote must not lead out of the order array
+      lo = max(p.offsets[e0 + lane], 0);
+      hi = static_cast<int>(min(static_cast<int64_t>(p.offsets[e0 + lane + 1]), p.M));
+    }
+    const int mine = hi > lo ? (hi - lo - 1) / bt + 1 : 0;
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    const int rel = block - before;
+    const unsigned hit = __ballot_sync(0xffffffffu, rel >= inc - mine && rel < inc);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int first = __shfl_sync(0xffffffffu, lo, src) + (rel - __shfl_sync(0xffffffffu, inc - mine, src)) * bt;
+      const int left = __shfl_sync(0xffffffffu, hi, src) - first;
+      *start = first;
+      *count = left < bt ? left : bt;
+      return e0 + src;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return -1;
+}
+
+}  // namespace sq
