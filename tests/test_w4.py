@@ -218,7 +218,8 @@ def test_linear(cuda_device, M, N, K, group, zero):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (4, 64, 49152), (16, 1000, 12288), (32, 49152, 256),
-                                   (128, 512, 4096), (1000, 777, 4112), (2048, 256, 512)])
+                                   (128, 512, 4096), (1000, 777, 4112), (2048, 256, 512), (640, 7700, 144),
+                                   (1280, 4000, 1040), (40, 130, 8208)])
 def test_linear_larger(cuda_device, M, N, K):
     rng = np.random.default_rng(M + N + K)
     _check_linear(_tokens(rng, M, K), ref.random_weight(rng, N, K, 128, M % 3 == 1), 128)

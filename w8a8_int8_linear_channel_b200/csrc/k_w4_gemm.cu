@@ -13,29 +13,42 @@
 // shared memory and reading it back as the MMA's operand would take twice the
 // shared-memory bandwidth that a tile's time leaves.
 //
-// Roles: eight dequantization warps (also the epilogue), four that copy token
-// rows (cp.async: gathered rows, K tails and missing tokens need no other
-// form), one MMA issuer, one record producer.  All waits are bounded.
+// Roles: eight or sixteen dequantization warps (also the epilogue), one MMA
+// issuer, one producer of records (bulk copies), and for the token rows one
+// TMA producer, or four warps of cp.async where an expert's rows lie scattered.
+// All waits are bounded.
+//
+// Tensor memory never has to be waited for: a CTA takes 256 columns and its
+// shared memory lets two of them share an SM, or 512 and one.
+#include "sq_tmap.h"
 #include "sq_w4.cuh"
 
 namespace sq {
 namespace {
 
-constexpr int kDequantWarps = 8;
-constexpr int kLoadWarps = 4;
-constexpr int kMmaWarp = kDequantWarps + kLoadWarps;
-constexpr int kRecordWarp = kMmaWarp + 1;
-constexpr int kThreads = (kRecordWarp + 1) * 32;
 constexpr int kMaxSlices = 8;
 constexpr int kACols = kW4K / 2;  // 32-bit TMEM columns of one 128 x 128 fp16 operand
 
-// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 operands, fp32 accumulate.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+// One lane of the warp (the same on every call).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, fp16 operands, fp32 accumulate, issued by
+// the lane with `leader` set.  The whole warp runs the issuing code, so its
+// operands stay in uniform registers: inside an `if (lane == 0)` an MMA of 16
+// tokens took 44 cycles to issue, this way 9 (32 tokens 16, 64 tokens 32: the
+// tensor core's own rate).
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc,
+                                           uint32_t leader) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b_desc), "r"(idesc), "r"(acc)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b_desc), "r"(idesc), "r"(acc), "r"(leader)
       : "memory");
 }
 
@@ -78,11 +91,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// Arrive on `bar` (one of its expected arrivals) when this thread's copies so
+// far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
@@ -92,14 +106,18 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, f
 // BT tokens and RT weight tiles (128 channels each) per CTA.
 template <int BT, int RT, int G, bool ZERO>
 struct Layout {
+  static constexpr int DEQ = RT == 2 ? 16 : 8;  // dequantization warps: RT weight tiles x even / odd K tiles
+  static constexpr int MMA_WARP = DEQ, REC_WARP = DEQ + 1, X_WARP = DEQ + 2;
+  static constexpr int X_THREADS = 128;  // of the cp.async form
+  static constexpr int THREADS = X_WARP * 32 + X_THREADS;
   static constexpr int REC = w4_record_bytes(G, ZERO);
   static constexpr int XSTAGE = BT * kW4K * 2;             // two boxes of [BT][64 k], 128-byte swizzle
-  static constexpr int XS = BT <= 32 ? 4 : RT == 2 ? 4 : 3;  // token stages
-  static constexpr int RS = RT == 2 ? 3 : 4;               // record stages, RT records each
-  static constexpr int AS = RT == 2 ? 2 : 3;               // operand buffers in tensor memory
+  static constexpr int XS = BT <= 64 ? 4 : RT == 2 ? 4 : 2;  // token stages
+  static constexpr int RS = RT == 2 ? 3 : BT <= 32 ? 7 : 4;  // record stages, RT records each
+  static constexpr int AS = RT == 2 || BT == 128 ? 2 : 3;  // operand buffers in tensor memory
   static constexpr int D_COLS = RT * BT;
   static constexpr int A0 = D_COLS;
-  static constexpr int TMEM_COLS = D_COLS + AS * RT * kACols <= 256 ? 256 : 512;
+  static constexpr int TMEM_COLS = RT == 2 ? 512 : 256;
   static constexpr int RED_PITCH = BT + 4;
   static constexpr int RED_BYTES = (kW4Rows + kMaxSlices) * RED_PITCH * 4;
   // the cluster's sums reuse the token stages: by then every MMA has read them
@@ -108,16 +126,19 @@ struct Layout {
   static constexpr int BARS = R + RS * RT * REC;
   static constexpr int NBARS = 2 * XS + 2 * RS + 2 * AS + 1;
   static constexpr int XROW = BARS + (NBARS * 8 + 15) / 16 * 16;  // int32 [BT]: x row of every token, -1 none
-  static constexpr int YROW = XROW + BT * 4;                      // int32 [BT]: y row
+  static constexpr int YROW = XROW + BT * 4;                      // int32 [BT]: y row, -1 none
   static constexpr int MISC = YROW + BT * 4;                      // abort, TMEM address, expert, count
   static constexpr int BYTES = MISC + 16 + 1024;                  // alignment slack
-  static_assert(D_COLS + AS * RT * kACols <= 512, "tensor memory");
+  static_assert(D_COLS + AS * RT * kACols <= TMEM_COLS, "tensor memory");
   static_assert(BYTES <= 232448, "shared memory per CTA");
+  static_assert(RT == 2 || (3 * (BYTES + 1024) > 233472 && 2 * (BYTES + 1024) <= 233472), "two CTAs per SM");
+  static_assert(RT == 1 || 2 * (BYTES + 1024) > 233472, "one CTA per SM");
 };
 
 template <int BT, int RT, int G, bool ZERO>
-__global__ void __launch_bounds__(kThreads, RT == 2 ? 1 : 2)
-    k_w4_gemm(const W4Product p, int slices, int blocks, int KT, uint32_t* status, uint64_t budget) {
+__global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 : 2)
+    k_w4_gemm(const __grid_constant__ CUtensorMap tmX, const W4Product p, int slices, int blocks, int KT,
+              uint32_t* status, uint64_t budget) {
   using L = Layout<BT, RT, G, ZERO>;
   constexpr int NG = kW4K / G;
   extern __shared__ uint8_t smem_raw[];
@@ -128,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, RT == 2 ? 1 : 2)
   int32_t* misc = reinterpret_cast<int32_t*>(smem + L::MISC);
   int32_t* xrow = reinterpret_cast<int32_t*>(smem + L::XROW);
   int32_t* yrow = reinterpret_cast<int32_t*>(smem + L::YROW);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const int slice = blockIdx.x % slices;
   const int block = blockIdx.x / slices % blocks;
   const int tile = blockIdx.x / slices / blocks * RT;  // first weight tile
@@ -138,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, RT == 2 ? 1 : 2)
   const uint32_t d_full = a_empty + 8 * L::AS;
 
   if (tid == 0) {
-    for (int s = 0; s < L::XS; ++s) mbar_init(x_full + 8 * s, kLoadWarps), mbar_init(x_empty + 8 * s, 1);
+    for (int s = 0; s < L::XS; ++s) mbar_init(x_full + 8 * s, p.offsets ? L::X_THREADS : 1), mbar_init(x_empty + 8 * s, 1);
     for (int s = 0; s < L::RS; ++s) {
       mbar_init(r_full + 8 * s, 1);
       mbar_init(r_empty + 8 * s, RT == 2 ? 8 : 4);
@@ -178,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, RT == 2 ? 1 : 2)
   __syncthreads();
   const int expert = misc[2], count = misc[3];
   if (expert < 0) return;  // the same for every CTA of the cluster
-  if (warp == kMmaWarp) {
+  if (warp == L::MMA_WARP) {
     tmem_alloc(smem_u32(misc + 1), L::TMEM_COLS);
     tmem_relinquish();
   }
@@ -191,16 +213,17 @@ __global__ void __launch_bounds__(kThreads, RT == 2 ? 1 : 2)
   const int n = static_cast<int>(static_cast<int64_t>(KT) * (slice + 1) / slices) - kt0;
   const int64_t nt = p.w.nt();
 
-  if (warp < kDequantWarps) {
-    // ---- dequantization: thread = channel; RT == 1: the two groups of four
-    // warps take even and odd K tiles, RT == 2: one weight tile each
-    const int group = warp >> 2;
+  if (warp < L::DEQ) {
+    // ---- dequantization: thread = channel; a group of four warps takes weight
+    // tile t and the K tiles of one parity
+    const int t = RT == 2 ? (warp >> 2) & 1 : 0;
+    const int parity = warp >> (RT == 2 ? 3 : 2);
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
-    for (int i = RT == 2 ? 0 : group; i < n; i += RT == 2 ? 1 : 2) {
+    for (int i = parity; i < n; i += 2) {
       const int rs = i % L::RS, as = i % L::AS;
-      if (!mbar_wait(r_full + 8 * rs, (i / L::RS) & 1, budget, status, abort)) break;
-      const int rec = L::R + (rs * RT + (RT == 2 ? group : 0)) * L::REC;
+      if (!w4_wait(r_full + 8 * rs, (i / L::RS) & 1, budget, status, abort)) break;
+      const int rec = L::R + (rs * RT + t) * L::REC;
       uint4 c[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) c[j] = lds128(sbase + rec + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
@@ -213,9 +236,9 @@ __global__ void __launch_bounds__(kThreads, RT == 2 ? 1 : 2)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(r_empty + 8 * rs);
-      if (i >= L::AS && !mbar_wait(a_empty + 8 * as, ((i / L::AS) & 1) ^ 1, budget, status, abort)) break;
+      if (i >= L::AS && !w4_wait(a_empty + 8 * as, ((i / L::AS) & 1) ^ 1, budget, status, abort)) break;
       tc_fence_after();
-      const uint32_t col = tmem + L::A0 + (as * RT + (RT == 2 ? group : 0)) * kACols + lanes;
+      const uint32_t col = tmem + L::A0 + (as * RT + t) * kACols + lanes;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const int j = w / (G / 32);
@@ -239,66 +262,42 @@ __global__ void __launch_bounds__(kThreads, RT == 2 ? 1 : 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(a_full + 8 * as);
     }
-  } else if (warp < kMmaWarp) {
-    // ---- token rows: 16 lanes copy a row's 128 k; arrival one tile late, so
-    // two tiles are in flight per thread
-    const int lt = tid - kDequantWarps * 32;
-    const int c = lt & 15;
-    const uint32_t box = static_cast<uint32_t>(c >> 3) * (BT * 128);
-    int done = 0;
+  } else if (warp == L::MMA_WARP) {
+    // ---- MMA issue (see mma_f16_ts: the whole warp, one lane elected)
+    constexpr uint32_t idesc = idesc_f16(kW4Rows, BT);
+    const uint32_t leader = elect_one();
+    const uint64_t desc0 = sdesc_k_sw128(sbase + L::X);
+    const bool short_tail = p.w.K - static_cast<int64_t>(kt0 + n - 1) * kW4K <= 64;  // one box in the last tile
+    uint32_t xs = 0, as = 0, xp = 0, ap = 0;
     for (int i = 0; i < n; ++i) {
-      const int xs = i % L::XS;
-      if (i >= L::XS && !mbar_wait(x_empty + 8 * xs, ((i / L::XS) & 1) ^ 1, budget, status, abort)) break;
-      const uint32_t stage = sbase + L::X + xs * L::XSTAGE + box;
-      const int64_t k = static_cast<int64_t>(kt0 + i) * kW4K + 8 * c;
+      if (!w4_wait(a_full + 8 * as, ap, budget, status, abort)) break;
+      if (!w4_wait(x_full + 8 * xs, xp, budget, status, abort)) break;
+      tc_fence_after();
+      if (p.offsets) fence_proxy_async_smem();  // cp.async rows, visible to this thread, to the MMA's reads
+      const uint64_t b0 = desc0 + xs * (L::XSTAGE >> 4);
+      const uint32_t a0 = tmem + L::A0 + as * (RT * kACols);
 #pragma unroll
-      for (int j = 0; j < BT / 8; ++j) {
-        const int row = (lt >> 4) + 8 * j;
-        const int32_t xr = xrow[row];
-        const bool live = xr >= 0 && k < p.w.K;
-        cp_async16(stage + row * 128 + (((c & 7) ^ (row & 7)) << 4), live ? p.x + xr * p.ldx + k : p.x, live ? 16 : 0);
+      for (int j = 0; j < 8; ++j) {
+        if (j == 4 && short_tail && i == n - 1) break;  // (the A columns past K are zero, the B rows were not copied)
+        const uint64_t b = b0 + (((j >> 2) * BT * 128 + (j & 3) * 32) >> 4);
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          mma_f16_ts(tmem + t * BT, a0 + t * kACols + 8 * j, b, idesc, i > 0 || j > 0, leader);
       }
-      cp_async_commit();
-      if (i > 0) {
-        cp_async_wait<1>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(x_full + 8 * (done % L::XS));
-        ++done;
-      }
-    }
-    cp_async_wait<0>();
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (done < n && lane == 0) mbar_arrive(x_full + 8 * (done % L::XS));
-  } else if (warp == kMmaWarp) {
-    // ---- MMA issue
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f16(kW4Rows, BT);
-      for (int i = 0; i < n; ++i) {
-        const int xs = i % L::XS, as = i % L::AS;
-        if (!mbar_wait(a_full + 8 * as, (i / L::AS) & 1, budget, status, abort)) break;
-        if (!mbar_wait(x_full + 8 * xs, (i / L::XS) & 1, budget, status, abort)) break;
-        tc_fence_after();
-        const uint64_t b0 = sdesc_k_sw128(sbase + L::X + xs * L::XSTAGE);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint64_t b = b0 + (((j >> 2) * BT * 128 + (j & 3) * 32) >> 4);
-#pragma unroll
-          for (int t = 0; t < RT; ++t)
-            mma_f16_ts(tmem + t * BT, tmem + L::A0 + (as * RT + t) * kACols + 8 * j, b, idesc, i > 0 || j > 0);
-        }
+      if (leader) {
         mma_commit(a_empty + 8 * as);
         mma_commit(x_empty + 8 * xs);
       }
-      mma_commit(d_full);  // also after a wait that ran out: nothing in flight is left behind
+      if (++xs == L::XS) xs = 0, xp ^= 1;
+      if (++as == L::AS) as = 0, ap ^= 1;
     }
-  } else if (lane == 0) {
+    if (leader) mma_commit(d_full);  // also after a wait that ran out: nothing in flight is left behind
+  } else if (warp == L::REC_WARP) {
     // ---- record producer
     int issued = 0;
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < n && lane == 0; ++i) {
       const int rs = i % L::RS;
-      if (i >= L::RS && !mbar_wait(r_empty + 8 * rs, ((i / L::RS) & 1) ^ 1, budget, status, abort)) break;
+      if (i >= L::RS && !w4_wait(r_empty + 8 * rs, ((i / L::RS) & 1) ^ 1, budget, status, abort)) break;
       // the last weight tile may stand alone: its place is taken by itself
       // again, and nothing of the copy is written out
       mbar_arrive_expect_tx(r_full + 8 * rs, RT * L::REC);
@@ -313,20 +312,71 @@ __global__ void __launch_bounds__(kThreads, RT == 2 ? 1 : 2)
     // records in flight land before the CTA can leave (at once unless a wait ran out)
     for (int i = max(0, issued - L::RS); i < issued; ++i)
       mbar_drain(r_full + 8 * (i % L::RS), (i / L::RS) & 1, budget);
+  } else if (p.offsets == nullptr) {
+    // ---- token rows of one matrix: TMA; rows past M and k past K read as zero
+    if (warp == L::X_WARP && lane == 0) {
+      int issued = 0;
+      uint32_t xs = 0, xp = 1;
+      for (int i = 0; i < n; ++i) {
+        if (i >= L::XS && !w4_wait(x_empty + 8 * xs, xp, budget, status, abort)) break;
+        const uint32_t stage = sbase + L::X + xs * L::XSTAGE, bar = x_full + 8 * xs;
+        const int32_t k = (kt0 + i) * kW4K;
+        // the second box of a short last tile may lie past K altogether: it is
+        // left out, and so are its MMAs
+        const int boxes = p.w.K - k > 64 ? 2 : 1;
+        mbar_arrive_expect_tx(bar, boxes * (BT * 128));
+        for (int b = 0; b < boxes; ++b) tma_load_2d(stage + b * (BT * 128), &tmX, bar, k + 64 * b, block * BT);
+        issued = i + 1;
+        if (++xs == L::XS) xs = 0, xp ^= 1;
+      }
+      // copies in flight land before the CTA can leave (at once unless a wait ran out)
+      for (int i = max(0, issued - L::XS); i < issued; ++i)
+        mbar_drain(x_full + 8 * (i % L::XS), (i / L::XS) & 1, budget);
+    }
+  } else {
+    // ---- an expert's token rows: 16 lanes copy a row's 128 k; each thread's
+    // arrival fires when its copies have landed, so the ring fills ahead
+    const int lt = tid - L::X_WARP * 32;
+    const int c = lt & 15;
+    const uint32_t at = static_cast<uint32_t>(c >> 3) * (BT * 128) + (lt >> 4) * 128 + (((c & 7) ^ ((lt >> 4) & 7)) << 4);
+    const __half* src[BT / 8];  // rows lt / 16 + 8 j: row & 7 does not depend on j
+    uint32_t live = 0;
+#pragma unroll
+    for (int j = 0; j < BT / 8; ++j) {
+      const int32_t xr = xrow[(lt >> 4) + 8 * j];
+      if (xr >= 0) live |= 1u << j;
+      src[j] = p.x + static_cast<int64_t>(xr >= 0 ? xr : 0) * p.ldx + static_cast<int64_t>(kt0) * kW4K + 8 * c;
+    }
+    int64_t left = p.w.K - static_cast<int64_t>(kt0) * kW4K - 8 * c;
+    uint32_t xs = 0, xp = 1;
+    for (int i = 0; i < n; ++i) {
+      if (i >= L::XS && !w4_wait(x_empty + 8 * xs, xp, budget, status, abort)) break;
+      const uint32_t dst = sbase + L::X + xs * L::XSTAGE + at;
+      const uint32_t mask = left > 0 ? live : 0;  // past K: zeros, and no address is read
+#pragma unroll
+      for (int j = 0; j < BT / 8; ++j) {
+        const bool on = mask >> j & 1;
+        cp_async16(dst + j * 1024, on ? src[j] : p.x, on ? 16 : 0);
+        src[j] += kW4K;
+      }
+      left -= kW4K;
+      cp_async_arrive(x_full + 8 * xs);
+      if (++xs == L::XS) xs = 0, xp ^= 1;
+    }
+    cp_async_wait_all();
   }
   __syncwarp();
 
   // ---- epilogue
-  mbar_drain(d_full, 0, budget);
+  mbar_wait_bounded(d_full, 0, budget > 100000000ull ? budget : 100000000ull);
   tc_fence_after();
   griddep_launch_dependents();
   if (slices > 1) cluster_sync_all();  // the token stages of every CTA are free
-  if (warp < kDequantWarps) {
-    const int group = warp >> 2;
+  if (warp < L::DEQ) {
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-    const int t = RT == 2 ? group : 0;
-    const int c0 = RT == 2 ? 0 : group * (BT / 2), c1 = RT == 2 ? BT : c0 + BT / 2;
+    const int t = RT == 2 ? (warp >> 2) & 1 : 0;
+    const int c0 = (warp >> (RT == 2 ? 3 : 2)) * (BT / 2), c1 = c0 + BT / 2;
     const int64_t ch = static_cast<int64_t>(tile + t) * kW4Rows + r;
     float bias = 0.0f;
     if (p.bias && ch < p.w.N) bias = __half2float(p.bias[static_cast<int64_t>(expert) * p.w.N + ch]);
@@ -369,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, RT == 2 ? 1 : 2)
     const int64_t n0 = static_cast<int64_t>(tile) * kW4Rows + slice * share;
     const int64_t left = min(p.w.N - n0, static_cast<int64_t>(kW4Rows - slice * share));
     const int width = static_cast<int>(left < share ? left : share);
-    for (int i = tid; i < width * count; i += kThreads) {
+    for (int i = tid; i < width * count; i += L::THREADS) {
       const int tk = i / width, q = i - tk * width;
       const int32_t row = yrow[tk];
       if (row < 0) continue;
@@ -387,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, RT == 2 ? 1 : 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, L::TMEM_COLS);
+  if (warp == L::MMA_WARP) tmem_dealloc(tmem, L::TMEM_COLS);
 }
 
 template <int BT, int RT, int G, bool ZERO>
@@ -396,13 +446,15 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   auto kernel = k_w4_gemm<BT, RT, G, ZERO>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return e;
+  CUtensorMap tm = {};
+  if (!p.offsets && !make_tmap_f16_rows(&tm, p.x, p.M, p.w.K, p.ldx, BT)) return cudaErrorUnknown;
   const int64_t tiles = (p.w.nt() + RT - 1) / RT, kt = p.w.kt();
   const int64_t blocks = w4_blocks(p, BT);
   const int slices = RT == 2 ? 1 : w4_slices(tiles * blocks, kt, static_cast<int64_t>(c.num_sms) * 2, 6);
   if (tiles * blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * blocks * slices));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(L::THREADS);
   cfg.dynamicSmemBytes = L::BYTES;
   cfg.stream = c.stream;
   cudaLaunchAttribute attr[2];
@@ -414,7 +466,7 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, slices, static_cast<int>(blocks), static_cast<int>(kt), c.status,
+  return cudaLaunchKernelEx(&cfg, kernel, tm, p, slices, static_cast<int>(blocks), static_cast<int>(kt), c.status,
                             c.budget_ns);
 }
 
@@ -436,7 +488,9 @@ cudaError_t launch_w4_gemm(const W4Product& p, const Ctx& c, int64_t tokens) {
   if (tokens <= 16) return launch_g<16, 1>(p, c);
   if (tokens <= 32) return launch_g<32, 1>(p, c);
   if (tokens <= 64) return launch_g<64, 1>(p, c);
-  return launch_g<128, 2>(p, c);
+  // two weight tiles per CTA halve the token traffic, if enough CTAs are left
+  if (w4_blocks(p, 128) * ((p.w.nt() + 1) / 2) >= c.num_sms) return launch_g<128, 2>(p, c);
+  return launch_g<128, 1>(p, c);
 }
 
 }  // namespace sq

@@ -120,7 +120,7 @@ sq_status sq_w4a16_experts(const void* x_f16, int64_t rows, int64_t ldx, const v
   if (st != SQ_OK) return st;
   if ((st = check_weight(w4, N, K, group, has_zero, &p.w)) != SQ_OK) return st;
   if (ldx < K) return SQ_ERR_INVALID_ARG;
-  if (pairs > 0x7fffffffLL || pairs_per_row > 0x7fffffffLL) return SQ_ERR_UNSUPPORTED_SHAPE;
+  if (rows > 0x7fffffffLL || pairs > 0x7fffffffLL || pairs_per_row > 0x7fffffffLL) return SQ_ERR_UNSUPPORTED_SHAPE;
   if ((pairs - 1) / pairs_per_row >= rows) return SQ_ERR_INVALID_ARG;  // the last pair's row does not exist
   if (ldx % 8 != 0 || !aligned16(x_f16) || !aligned16(bias_f16) || !aligned16(y) || !aligned16(offsets) ||
       !aligned16(order))

@@ -44,6 +44,22 @@ inline bool make_tmap_f16_out(CUtensorMap* map, const void* base, uint64_t cols,
   return r == CUDA_SUCCESS;
 }
 
+// rows x K fp16 matrix (row stride ld elements, a multiple of 8); boxes of 64
+// elements x box_rows rows, 128-byte swizzle.
+inline bool make_tmap_f16_rows(CUtensorMap* map, const void* base, uint64_t rows, uint64_t K, uint64_t ld,
+                               uint32_t box_rows) {
+  auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!encode) return false;
+  cuuint64_t dims[2] = {K, rows};
+  cuuint64_t strides[1] = {ld * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t elem[2] = {1, 1};
+  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims, strides,
+                      box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 }  // namespace sq
 
 namespace sq {

@@ -14,6 +14,24 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
+// mbar_wait whose tries suspend the warp (up to 2 us each) instead of polling:
+// with fourteen warps on a scheduler's issue slots the waiting ones must not
+// take any.
+__device__ __forceinline__ bool w4_wait(uint32_t bar, uint32_t parity, uint64_t budget_ns, uint32_t* status,
+                                        volatile uint32_t* abort) {
+  if (mbar_try_wait_hint(bar, parity, 2000)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_hint(bar, parity, 2000)) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > budget_ns) {
+      atomicCAS(status, DEV_OK, DEV_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
