@@ -261,6 +261,45 @@ def test_experts(cuda_device, T, topk, E, N, K, group, zero):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,topk,E,N,K", [(1024, 8, 64, 512, 2048), (24, 4, 64, 512, 4096), (200, 4, 32, 640, 2048)])
+def test_experts_back_to_back(cuda_device, T, topk, E, N, K):
+    """Many launches in a row, overlapping at their ends, over weights that do not stay in L2: the
+    same bits as from single launches."""
+    import w8a8_int8_linear_channel_b200 as sq
+    rng = np.random.default_rng(T)
+    P = T * topk
+    w4 = [_pack(ref.random_weight(np.random.default_rng(i), N, K, 128, False, lead=(1,)), 128) for i in range(2)]
+    ws = []
+    for i in range(4):  # four packed weights of E experts each, made of two experts' bytes in turn
+        w = sq.new_w4_weight(N, K, 128, experts=E)
+        n = w.packed.numel() // E
+        for e in range(E):
+            w.packed[e * n:(e + 1) * n] = w4[(e + i) & 1].packed
+        ws.append(w)
+    x = dev(_tokens(rng, T, K))
+    ids = dev(np.stack([rng.permutation(E)[:topk] for _ in range(T)]).astype(np.int32))
+    off = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    order = torch.empty(P, dtype=torch.int32, device="cuda")
+    sq.sq_moe_plan(ids, off, order)
+    want = []
+    for w in ws:
+        want.append(sq.sq_w4a16_experts(x, w, off, order, torch.empty((P, N), dtype=torch.float16, device="cuda"), topk))
+        torch.cuda.synchronize()
+    junk = torch.empty(200 << 20, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty((P, N), dtype=torch.float16, device="cuda") for _ in range(40)]
+    junk.fill_(1)
+    for i, y in enumerate(outs):
+        sq.sq_w4a16_experts(x, ws[i % 4], off, order, y, topk)
+    assert sq.sq_poll_status() == 0
+    for i, y in enumerate(outs):
+        assert torch.equal(y, want[i % 4])
+    W = ref.values(*ref.random_weight(np.random.default_rng(0), N, K, 128, False, lead=(1,)), 128)[0]
+    pairs = np.nonzero(host(ids).reshape(-1) == 0)[0][:8]
+    y0, bound = ref.linear(host(x)[pairs // topk], W)
+    assert (np.abs(host(want[0])[pairs].astype(np.float64) - y0) <= bound).all()
+
+
+@pytest.mark.gpu
 def test_experts_skip_entries_no_plan_wrote(cuda_device):
     """Offsets and orders outside the pairs lead nowhere: nothing is read or written for them."""
     import w8a8_int8_linear_channel_b200 as sq

@@ -113,7 +113,7 @@ struct Layout {
   static constexpr int REC = w4_record_bytes(G, ZERO);
   static constexpr int XSTAGE = BT * kW4K * 2;             // two boxes of [BT][64 k], 128-byte swizzle
   static constexpr int XS = BT <= 64 ? 4 : RT == 2 ? 4 : 2;  // token stages
-  static constexpr int RS = RT == 2 ? 3 : BT <= 32 ? 7 : 4;  // record stages, RT records each
+  static constexpr int RS = BT <= 32 ? 7 : 4;               // record stages, RT records each
   static constexpr int AS = RT == 2 || BT == 128 ? 2 : 3;  // operand buffers in tensor memory
   static constexpr int D_COLS = RT * BT;
   static constexpr int A0 = D_COLS;
@@ -130,6 +130,12 @@ struct Layout {
   static constexpr int MISC = YROW + BT * 4;                      // abort, TMEM address, expert, count
   static constexpr int BYTES = MISC + 16 + 1024;                  // alignment slack
   static_assert(D_COLS + AS * RT * kACols <= TMEM_COLS, "tensor memory");
+  // The parity of a barrier's phase tells two successive uses of a stage
+  // apart, not three.  A group of warps (K tiles of one parity) that asks for
+  // tile j has seen the MMAs of tile j - 2 - AS done, so that tile had landed;
+  // tile j - RS, the stage's use before, must not be a later one, unless it is
+  // the same group's (RS even).
+  static_assert(RS % 2 == 0 || RS >= AS + 2, "a wait could take the phase before the last for its own");
   static_assert(BYTES <= 232448, "shared memory per CTA");
   static_assert(RT == 2 || (3 * (BYTES + 1024) > 233472 && 2 * (BYTES + 1024) <= 233472), "two CTAs per SM");
   static_assert(RT == 1 || 2 * (BYTES + 1024) > 233472, "one CTA per SM");
@@ -201,6 +207,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   const int expert = misc[2], count = misc[3];
   if (expert < 0) return;  // the same for every CTA of the cluster
   if (warp == L::MMA_WARP) {
+    __syncwarp();
     tmem_alloc(smem_u32(misc + 1), L::TMEM_COLS);
     tmem_relinquish();
   }
@@ -222,7 +229,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
     for (int i = parity; i < n; i += 2) {
       const int rs = i % L::RS, as = i % L::AS;
-      if (!w4_wait(r_full + 8 * rs, (i / L::RS) & 1, budget, status, abort)) break;
+      if (!w4_wait_warp(r_full + 8 * rs, (i / L::RS) & 1, budget, status, abort)) break;
       const int rec = L::R + (rs * RT + t) * L::REC;
       uint4 c[4];
 #pragma unroll
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(r_empty + 8 * rs);
-      if (i >= L::AS && !w4_wait(a_empty + 8 * as, ((i / L::AS) & 1) ^ 1, budget, status, abort)) break;
+      if (i >= L::AS && !w4_wait_warp(a_empty + 8 * as, ((i / L::AS) & 1) ^ 1, budget, status, abort)) break;
       tc_fence_after();
       const uint32_t col = tmem + L::A0 + (as * RT + t) * kACols + lanes;
 #pragma unroll
@@ -270,8 +277,8 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     const bool short_tail = p.w.K - static_cast<int64_t>(kt0 + n - 1) * kW4K <= 64;  // one box in the last tile
     uint32_t xs = 0, as = 0, xp = 0, ap = 0;
     for (int i = 0; i < n; ++i) {
-      if (!w4_wait(a_full + 8 * as, ap, budget, status, abort)) break;
-      if (!w4_wait(x_full + 8 * xs, xp, budget, status, abort)) break;
+      if (!w4_wait_warp(a_full + 8 * as, ap, budget, status, abort)) break;
+      if (!w4_wait_warp(x_full + 8 * xs, xp, budget, status, abort)) break;
       tc_fence_after();
       if (p.offsets) fence_proxy_async_smem();  // cp.async rows, visible to this thread, to the MMA's reads
       const uint64_t b0 = desc0 + xs * (L::XSTAGE >> 4);
@@ -350,7 +357,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     int64_t left = p.w.K - static_cast<int64_t>(kt0) * kW4K - 8 * c;
     uint32_t xs = 0, xp = 1;
     for (int i = 0; i < n; ++i) {
-      if (i >= L::XS && !w4_wait(x_empty + 8 * xs, xp, budget, status, abort)) break;
+      if (i >= L::XS && !w4_wait_warp(x_empty + 8 * xs, xp, budget, status, abort)) break;
       const uint32_t dst = sbase + L::X + xs * L::XSTAGE + at;
       const uint32_t mask = left > 0 ? live : 0;  // past K: zeros, and no address is read
 #pragma unroll
@@ -369,6 +376,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
 
   // ---- epilogue
   mbar_wait_bounded(d_full, 0, budget > 100000000ull ? budget : 100000000ull);
+  __syncwarp();
   tc_fence_after();
   griddep_launch_dependents();
   if (slices > 1) cluster_sync_all();  // the token stages of every CTA are free
@@ -384,6 +392,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     constexpr int STEP = 8;
     for (int col = c0; col < c1; col += STEP) {
       if (col >= count) break;  // no token of this block lies there
+      __syncwarp();
       uint32_t v[8];
       tmem_ld_x8(tmem + t * BT + col + lanes, v);
       if (slices > 1) {
@@ -412,6 +421,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       }
     }
   }
+  __syncwarp();
   if (slices > 1) {
     cluster_sync_all();  // releases the pushes; nothing of this CTA is touched from outside after it
     const int share = (kW4Rows + slices - 1) / slices;
@@ -435,6 +445,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
         p.y32[o] = f;
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == L::MMA_WARP) tmem_dealloc(tmem, L::TMEM_COLS);

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads)
     const int live = __popc(__ballot_sync(0xffffffffu, xrow != nullptr));
     uint32_t stage = sbase, bar = full, phase = 1;
     for (int i = 0; i < n; ++i) {
-      if (i >= L::STAGES && !w4_wait(bar + 8 * L::STAGES, phase, budget, status, abort)) break;
+      if (i >= L::STAGES && !w4_wait_warp(bar + 8 * L::STAGES, phase, budget, status, abort)) break;
       const uint32_t xbytes = tail && kt0 + i == KT - 1 ? 2 * tail : 2 * kW4K;
       if (lane == 0) {
         mbar_arrive_expect_tx(bar, L::REC + live * xbytes);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int j = 0; j < 4; ++j) acc[m][b][j] = 0.0f;
     uint32_t s = kg, phase = 0;
     for (int i = kg; i < n; i += kKGroups) {
-      if (!w4_wait(full + 8 * s, phase, budget, status, abort)) break;
+      if (!w4_wait_warp(full + 8 * s, phase, budget, status, abort)) break;
       const uint32_t stage = sbase + s * L::STAGE;
       if (tail && kt0 + i == KT - 1)
         consume<NB, G, ZERO, true>(stage, smem + s * L::STAGE, r0, lane, tail, acc);
@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
   }
+  __syncwarp();
   griddep_launch_dependents();
   if (slices > 1)
     cluster_sync_all();  // releases the pushes; nothing of this CTA is touched from outside after it

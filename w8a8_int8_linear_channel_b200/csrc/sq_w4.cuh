@@ -32,6 +32,14 @@ __device__ __forceinline__ bool w4_wait(uint32_t bar, uint32_t parity, uint64_t 
   return true;
 }
 
+// The same by a whole warp, which is converged on return with one answer: the
+// .sync.aligned instructions (tcgen05, mma, barrier.cluster) that follow a wait
+// must not meet a warp whose lanes left the wait at different times.
+__device__ __forceinline__ bool w4_wait_warp(uint32_t bar, uint32_t parity, uint64_t budget_ns, uint32_t* status,
+                                             volatile uint32_t* abort) {
+  return __all_sync(0xffffffffu, w4_wait(bar, parity, budget_ns, status, abort));
+}
+
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
