@@ -70,14 +70,22 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Columns [col, col + 8) of the warp's lanes, complete on return.
-__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&r)[8]) {
+// Columns [col, col + 8 or 16) of the warp's lanes, complete on return.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr)
                : "memory");
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
+  tmem_ld_32x32b_x16(taddr, r);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
 }
@@ -137,6 +145,7 @@ struct Layout {
   // the same group's (RS even).
   static_assert(RS % 2 == 0 || RS >= AS + 2, "a wait could take the phase before the last for its own");
   static_assert(BYTES <= 232448, "shared memory per CTA");
+  static_assert(BT * (RT * kW4Rows * 4 + 16) <= BARS, "the staged output tile");
   static_assert(RT == 2 || (3 * (BYTES + 1024) > 233472 && 2 * (BYTES + 1024) <= 233472), "two CTAs per SM");
   static_assert(RT == 1 || 2 * (BYTES + 1024) > 233472, "one CTA per SM");
 };
@@ -227,9 +236,11 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     const int parity = warp >> (RT == 2 ? 3 : 2);
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
+    // stage and buffer counters in steps of two tiles (an `empty` barrier that
+    // nobody has used yet answers parity 1 at once)
+    uint32_t rs = parity, rp = 0, as = parity, ap = 1;
     for (int i = parity; i < n; i += 2) {
-      const int rs = i % L::RS, as = i % L::AS;
-      if (!w4_wait_warp(r_full + 8 * rs, (i / L::RS) & 1, budget, status, abort)) break;
+      if (!w4_wait_warp(r_full + 8 * rs, rp, budget, status, abort)) break;
       const int rec = L::R + (rs * RT + t) * L::REC;
       uint4 c[4];
 #pragma unroll
@@ -243,7 +254,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(r_empty + 8 * rs);
-      if (i >= L::AS && !w4_wait_warp(a_empty + 8 * as, ((i / L::AS) & 1) ^ 1, budget, status, abort)) break;
+      if (!w4_wait_warp(a_empty + 8 * as, ap, budget, status, abort)) break;
       tc_fence_after();
       const uint32_t col = tmem + L::A0 + (as * RT + t) * kACols + lanes;
 #pragma unroll
@@ -268,6 +279,8 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(a_full + 8 * as);
+      if ((rs += 2) >= L::RS) rs -= L::RS, rp ^= 1;
+      if ((as += 2) >= L::AS) as -= L::AS, ap ^= 1;
     }
   } else if (warp == L::MMA_WARP) {
     // ---- MMA issue (see mma_f16_ts: the whole warp, one lane elected)
@@ -302,9 +315,9 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   } else if (warp == L::REC_WARP) {
     // ---- record producer
     int issued = 0;
+    uint32_t rs = 0, rp = 1;
     for (int i = 0; i < n && lane == 0; ++i) {
-      const int rs = i % L::RS;
-      if (i >= L::RS && !w4_wait(r_empty + 8 * rs, ((i / L::RS) & 1) ^ 1, budget, status, abort)) break;
+      if (!w4_wait(r_empty + 8 * rs, rp, budget, status, abort)) break;
       // the last weight tile may stand alone: its place is taken by itself
       // again, and nothing of the copy is written out
       mbar_arrive_expect_tx(r_full + 8 * rs, RT * L::REC);
@@ -315,6 +328,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
                   p.w.data + ((static_cast<int64_t>(expert) * nt + wt) * KT + kt0 + i) * L::REC, L::REC, r_full + 8 * rs);
       }
       issued = i + 1;
+      if (++rs == L::RS) rs = 0, rp ^= 1;
     }
     // records in flight land before the CTA can leave (at once unless a wait ran out)
     for (int i = max(0, issued - L::RS); i < issued; ++i)
@@ -325,7 +339,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       int issued = 0;
       uint32_t xs = 0, xp = 1;
       for (int i = 0; i < n; ++i) {
-        if (i >= L::XS && !w4_wait(x_empty + 8 * xs, xp, budget, status, abort)) break;
+        if (!w4_wait(x_empty + 8 * xs, xp, budget, status, abort)) break;
         const uint32_t stage = sbase + L::X + xs * L::XSTAGE, bar = x_full + 8 * xs;
         const int32_t k = (kt0 + i) * kW4K;
         // the second box of a short last tile may lie past K altogether: it is
@@ -357,7 +371,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     int64_t left = p.w.K - static_cast<int64_t>(kt0) * kW4K - 8 * c;
     uint32_t xs = 0, xp = 1;
     for (int i = 0; i < n; ++i) {
-      if (i >= L::XS && !w4_wait_warp(x_empty + 8 * xs, xp, budget, status, abort)) break;
+      if (!w4_wait_warp(x_empty + 8 * xs, xp, budget, status, abort)) break;
       const uint32_t dst = sbase + L::X + xs * L::XSTAGE + at;
       const uint32_t mask = left > 0 ? live : 0;  // past K: zeros, and no address is read
 #pragma unroll
@@ -380,6 +394,13 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   tc_fence_after();
   griddep_launch_dependents();
   if (slices > 1) cluster_sync_all();  // the token stages of every CTA are free
+  // Without slices a tile goes out through shared memory (every stage is free
+  // by now), so that a warp writes 512 consecutive bytes of a row; written
+  // from the accumulators' own layout, 32 channels of one token per store, a
+  // 128 x 256 tile took 5.5 us.
+  const int es = p.y ? 2 : 4;
+  const bool staged = slices == 1 && (p.w.N * es) % 16 == 0;
+  const uint32_t pitch = RT * kW4Rows * es + 16;
   if (warp < L::DEQ) {
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
@@ -389,12 +410,12 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     float bias = 0.0f;
     if (p.bias && ch < p.w.N) bias = __half2float(p.bias[static_cast<int64_t>(expert) * p.w.N + ch]);
     const int share = (kW4Rows + slices - 1) / slices;
-    constexpr int STEP = 8;
+    constexpr int STEP = BT == 16 ? 8 : 16;
     for (int col = c0; col < c1; col += STEP) {
       if (col >= count) break;  // no token of this block lies there
       __syncwarp();
-      uint32_t v[8];
-      tmem_ld_x8(tmem + t * BT + col + lanes, v);
+      uint32_t v[STEP];
+      tmem_ld_cols(tmem + t * BT + col + lanes, v);
       if (slices > 1) {
         const int owner = r / share;
         const uint32_t at =
@@ -407,18 +428,40 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       } else {
 #pragma unroll
         for (int j = 0; j < STEP; ++j) {
-          const int32_t row = yrow[col + j];
-          if (row < 0 || ch >= p.w.N) continue;
           float f = __uint_as_float(v[j]);
           if (p.bias) f = __fadd_rn(f, bias);
           if (p.relu) f = f > 0.0f ? f : 0.0f;
-          const int64_t o = static_cast<int64_t>(row) * p.w.N + ch;
-          if (p.y)
-            p.y[o] = __float2half_rn(f);
-          else
-            p.y32[o] = f;
+          if (staged) {
+            uint8_t* at = smem + (col + j) * pitch + (t * kW4Rows + r) * es;
+            if (p.y)
+              *reinterpret_cast<__half*>(at) = __float2half_rn(f);
+            else
+              *reinterpret_cast<float*>(at) = f;
+          } else {
+            const int32_t row = yrow[col + j];
+            if (row < 0 || ch >= p.w.N) continue;
+            const int64_t o = static_cast<int64_t>(row) * p.w.N + ch;
+            if (p.y)
+              p.y[o] = __float2half_rn(f);
+            else
+              p.y32[o] = f;
+          }
         }
       }
+    }
+  }
+  if (staged) {
+    __syncthreads();
+    // 16-byte pieces; a row's pieces go to consecutive lanes
+    const int per = RT * kW4Rows * es / 16;  // a power of two
+    const int shift = __ffs(per) - 1;
+    uint8_t* out = p.y ? reinterpret_cast<uint8_t*>(p.y) : reinterpret_cast<uint8_t*>(p.y32);
+    const int64_t row_bytes = p.w.N * es, first = static_cast<int64_t>(tile) * kW4Rows * es;
+    for (int i = tid; i < count << shift; i += L::THREADS) {
+      const int tk = i >> shift, c = (i & (per - 1)) * 16;
+      const int32_t row = yrow[tk];
+      if (row < 0 || first + c >= row_bytes) continue;
+      *reinterpret_cast<uint4*>(out + row * row_bytes + first + c) = *reinterpret_cast<const uint4*>(smem + tk * pitch + c);
     }
   }
   __syncwarp();
@@ -455,13 +498,16 @@ template <int BT, int RT, int G, bool ZERO>
 cudaError_t launch(const W4Product& p, const Ctx& c) {
   using L = Layout<BT, RT, G, ZERO>;
   auto kernel = k_w4_gemm<BT, RT, G, ZERO>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  static KernelSetup setup;
+  int per_sm = 0;
+  const cudaError_t e =
+      kernel_setup(setup, reinterpret_cast<const void*>(kernel), L::THREADS, L::BYTES, c.device, &per_sm);
   if (e != cudaSuccess) return e;
   CUtensorMap tm = {};
   if (!p.offsets && !make_tmap_f16_rows(&tm, p.x, p.M, p.w.K, p.ldx, BT)) return cudaErrorUnknown;
   const int64_t tiles = (p.w.nt() + RT - 1) / RT, kt = p.w.kt();
   const int64_t blocks = w4_blocks(p, BT);
-  const int slices = RT == 2 ? 1 : w4_slices(tiles * blocks, kt, static_cast<int64_t>(c.num_sms) * 2, 6);
+  const int slices = RT == 2 ? 1 : w4_slices(tiles * blocks, kt, static_cast<int64_t>(c.num_sms) * per_sm, 6);
   if (tiles * blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * blocks * slices));

@@ -322,13 +322,13 @@ template <int NB, int G, bool ZERO>
 cudaError_t launch(const W4Product& p, const Ctx& c) {
   using L = Layout<NB, G, ZERO>;
   auto kernel = k_w4_stream<NB, G, ZERO>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  static KernelSetup setup;
+  int per_sm = 0;
+  const cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(kernel), kThreads, L::BYTES, c.device, &per_sm);
   if (e != cudaSuccess) return e;
   const int64_t nt = p.w.nt(), kt = p.w.kt();
   const int64_t blocks = w4_blocks(p, L::BT);
-  int per_sm = 0;
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, L::BYTES)) != cudaSuccess) return e;
-  const int slices = w4_slices(nt * blocks, kt, static_cast<int64_t>(c.num_sms) * (per_sm > 0 ? per_sm : 1), 6);
+  const int slices = w4_slices(nt * blocks, kt, static_cast<int64_t>(c.num_sms) * per_sm, 6);
   cudaLaunchConfig_t cfg = {};
   if (nt * blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cfg.gridDim = dim3(static_cast<unsigned>(nt * blocks * slices));

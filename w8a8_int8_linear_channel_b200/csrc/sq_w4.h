@@ -3,6 +3,8 @@
 // and the kernel files.  Not part of the public ABI.
 #pragma once
 
+#include <atomic>
+
 #include "sq_internal.h"
 
 namespace sq {
@@ -39,6 +41,25 @@ struct W4Weight {
   __host__ __device__ int64_t kt() const { return (K + kW4K - 1) / kW4K; }
   int64_t bytes() const { return nt() * kt() * w4_record_bytes(group, zero); }
 };
+
+// Per kernel and device, once: allows `smem` bytes of dynamic shared memory and
+// counts the resident CTAs per SM.  A launch of a few microseconds should not
+// ask the runtime for either every time.
+struct KernelSetup {
+  std::atomic<int> per_sm[64];  // 0: not asked yet
+};
+inline cudaError_t kernel_setup(KernelSetup& k, const void* kernel, int threads, size_t smem, int device, int* per_sm) {
+  int n = k.per_sm[device].load(std::memory_order_acquire);
+  if (n == 0) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorLaunchOutOfResources;
+    k.per_sm[device].store(n, std::memory_order_release);
+  }
+  *per_sm = n;
+  return cudaSuccess;
+}
 
 cudaError_t launch_w4_pack(const uint8_t* codes, const __half* scales, const uint8_t* zeros, const W4Weight& w,
                            const Ctx& c);

@@ -12,11 +12,32 @@ from typing import Optional
 
 import torch
 
-from . import _L, _check, _p, _rows, _stream, _vec
+from . import _L, _check, _p, _rows, _vec
 
 MOE_MAX_EXPERTS = 512
 MOE_MAX_TOPK = 32
 GROUPS = (32, 64, 128)
+
+
+# These calls take a few microseconds on the GPU, so their host side counts: one
+# look at the current device per call, plain integers as pointers, and the
+# current stream's handle without a Stream object where torch offers it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _ptrs(*tensors):
+    """Device addresses (None stays None); a host tensor or one on another GPU is refused as by _p."""
+    first = next(t for t in tensors if t is not None)
+    dev = torch.cuda.current_device() if first.is_cuda else -2
+    return [None if t is None else (t.data_ptr() if t.get_device() == dev else _p(t)) for t in tensors]
+
+
+def _stream(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 class W4Weight:
@@ -58,9 +79,9 @@ def _dense(w4: W4Weight, what: str) -> None:
         raise ValueError(f"{what}: a single weight is needed, this one holds {w4.experts} experts")
 
 
-def _tensor(t: torch.Tensor, dtype, shape, name: str) -> None:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name}: need a contiguous {dtype} {tuple(shape)} tensor")
+def _tensor(t: torch.Tensor, dtype, shape: tuple, name: str) -> None:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} {shape} tensor")
 
 
 def sq_quantize_weight_w4(w: torch.Tensor, w4: W4Weight, s=None, stream=None) -> W4Weight:
@@ -69,8 +90,9 @@ def sq_quantize_weight_w4(w: torch.Tensor, w4: W4Weight, s=None, stream=None) ->
     _tensor(w, torch.float16, lead + (w4.N, w4.K), "w")
     _vec(s, w4.K, torch.float32, "s")
     for src, dst in ((w, w4),) if w4.experts is None else ((w[e], w4[e]) for e in range(w4.experts)):
-        _check(_L.sq_quantize_weight_w4(_p(src), w4.N, w4.K, _p(s), w4.group, int(w4.zero_point), _p(dst.packed),
-                                        _stream(stream)), "sq_quantize_weight_w4")
+        a, b, c = _ptrs(src, s, dst.packed)
+        _check(_L.sq_quantize_weight_w4(a, w4.N, w4.K, b, w4.group, w4.zero_point, c, _stream(stream)),
+               "sq_quantize_weight_w4")
     return w4
 
 
@@ -92,7 +114,8 @@ def sq_w4_pack(codes: torch.Tensor, scales: torch.Tensor, w4: W4Weight, zeros=No
     for c, s, z, dst in parts:
         if s.data_ptr() % 16 or (z is not None and z.data_ptr() % 16):  # an expert's slice may start off 16 bytes
             s, z = s.clone(), None if z is None else z.clone()
-        _check(_L.sq_w4_pack(_p(c), _p(s), _p(z), w4.N, w4.K, w4.group, _p(dst.packed), _stream(stream)), "sq_w4_pack")
+        pc, ps, pz, pw = _ptrs(c, s, z, dst.packed)
+        _check(_L.sq_w4_pack(pc, ps, pz, w4.N, w4.K, w4.group, pw, _stream(stream)), "sq_w4_pack")
     return w4
 
 
@@ -100,8 +123,8 @@ def sq_w4_dequantize(w4: W4Weight, out: torch.Tensor, stream=None) -> torch.Tens
     """out fp16 [N, K] = the values of a packed weight."""
     _dense(w4, "sq_w4_dequantize")
     _tensor(out, torch.float16, (w4.N, w4.K), "out")
-    _check(_L.sq_w4_dequantize(_p(w4.packed), w4.N, w4.K, w4.group, int(w4.zero_point), _p(out), _stream(stream)),
-           "sq_w4_dequantize")
+    pw, po = _ptrs(w4.packed, out)
+    _check(_L.sq_w4_dequantize(pw, w4.N, w4.K, w4.group, w4.zero_point, po, _stream(stream)), "sq_w4_dequantize")
     return out
 
 
@@ -116,8 +139,9 @@ def sq_w4a16_linear(x: torch.Tensor, w4: W4Weight, y: torch.Tensor, bias=None, r
         ld = max(ld, K)  # the stride of a single row means nothing
     _vec(bias, w4.N, torch.float16, "bias")
     _tensor(y, torch.float16, (M, w4.N), "y")
-    _check(_L.sq_w4a16_linear(_p(x), M, ld, _p(w4.packed), w4.N, K, w4.group, int(w4.zero_point), _p(bias),
-                              int(bool(relu)), _p(y), _stream(stream)), "sq_w4a16_linear")
+    px, pw, pb, py = _ptrs(x, w4.packed, bias, y)
+    _check(_L.sq_w4a16_linear(px, M, ld, pw, w4.N, K, w4.group, w4.zero_point, pb, bool(relu), py, _stream(stream)),
+           "sq_w4a16_linear")
     return y
 
 
@@ -140,9 +164,10 @@ def sq_moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
     _tensor(ids, torch.int32, (T, topk), "ids")
     _tensor(weights, torch.float32, (T, topk), "weights")
     _vec(bias, E, torch.float32, "bias")
-    _check(_L.sq_moe_route(_p(logits), int(logits.dtype == torch.float16), T, E, max(ld, E) if T == 1 else ld,
-                           _p(bias), _SCORES[score], n_group, topk_group, group_top, topk, int(bool(renormalize)),
-                           scale, _p(ids), _p(weights), _stream(stream)), "sq_moe_route")
+    pl, pb, pi, pw = _ptrs(logits, bias, ids, weights)
+    _check(_L.sq_moe_route(pl, logits.dtype == torch.float16, T, E, max(ld, E) if T == 1 else ld, pb, _SCORES[score],
+                           n_group, topk_group, group_top, topk, bool(renormalize), scale, pi, pw, _stream(stream)),
+           "sq_moe_route")
     return ids, weights
 
 
@@ -164,8 +189,8 @@ def sq_moe_plan(ids: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor, w
             with torch.cuda.stream(stream):  # freed memory is reused in this stream's order
                 workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_L.sq_moe_plan(_p(ids), pairs, E, _p(offsets), _p(order), _p(workspace), ws_bytes, _stream(stream)),
-           "sq_moe_plan")
+    pi, pf, po, pw = _ptrs(ids, offsets, order, workspace)
+    _check(_L.sq_moe_plan(pi, pairs, E, pf, po, pw, ws_bytes, _stream(stream)), "sq_moe_plan")
     return offsets, order
 
 
@@ -188,9 +213,10 @@ def sq_w4a16_experts(x: torch.Tensor, w4: W4Weight, offsets: torch.Tensor, order
     if y.dtype not in (torch.float16, torch.float32):
         raise ValueError("y: fp16 or fp32")
     _tensor(y, y.dtype, (pairs, w4.N), "y")
-    _check(_L.sq_w4a16_experts(_p(x), rows, ld, _p(w4.packed), w4.experts, w4.N, K, w4.group, int(w4.zero_point),
-                               _p(bias), int(bool(relu)), _p(offsets), _p(order), pairs, pairs_per_row, _p(y),
-                               int(y.dtype == torch.float32), _stream(stream)), "sq_w4a16_experts")
+    px, pw, pb, pf, po, py = _ptrs(x, w4.packed, bias, offsets, order, y)
+    _check(_L.sq_w4a16_experts(px, rows, ld, pw, w4.experts, w4.N, K, w4.group, w4.zero_point, pb, bool(relu), pf, po,
+                               pairs, pairs_per_row, py, y.dtype == torch.float32, _stream(stream)),
+           "sq_w4a16_experts")
     return y
 
 
@@ -207,8 +233,9 @@ def sq_moe_combine(y_pairs: torch.Tensor, ids: torch.Tensor, weights: torch.Tens
     _tensor(weights, torch.float32, (T, topk), "weights")
     _tensor(y_pairs, y_pairs.dtype, (T * topk, N), "y_pairs")
     _tensor(y, torch.float16, (T, N), "y")
-    _check(_L.sq_moe_combine(_p(y_pairs), int(y_pairs.dtype == torch.float32), _p(ids), _p(weights), T, topk, N,
-                             experts, _p(y), _stream(stream)), "sq_moe_combine")
+    pz, pi, pw, py = _ptrs(y_pairs, ids, weights, y)
+    _check(_L.sq_moe_combine(pz, y_pairs.dtype == torch.float32, pi, pw, T, topk, N, experts, py, _stream(stream)),
+           "sq_moe_combine")
     return y
 
 
@@ -257,10 +284,16 @@ class W4Experts:
                  scale: float = 1.0, up_bias=None, down_bias=None):
         if up.experts is None or up.experts != down.experts or (up.N, up.K) != (down.K, down.N):
             raise ValueError("up / down: need [E, F, K] and [E, K, F] of the same experts")
+        if score not in _SCORES:
+            raise ValueError(f"score: one of {sorted(_SCORES)}")
+        _vec(router_bias, up.experts, torch.float32, "router_bias")
+        for t, w, name in ((up_bias, up, "up_bias"), (down_bias, down, "down_bias")):
+            if t is not None:
+                _tensor(t, torch.float16, (w.experts, w.N), name)
         self.up, self.down, self.topk = up, down, topk
         self.score, self.router_bias = score, router_bias
         self.n_group, self.topk_group, self.group_top = n_group, topk_group, group_top
-        self.renormalize, self.scale = renormalize, scale
+        self.renormalize, self.scale = bool(renormalize), scale
         self.up_bias, self.down_bias = up_bias, down_bias
 
     @classmethod
@@ -273,34 +306,44 @@ class W4Experts:
             packed.append(sq_quantize_weight_w4(w, w4))
         return cls(packed[0], packed[1], topk, **kw)
 
-    def route(self, logits: torch.Tensor):
-        """ids int32 and weights fp32, [T, topk], of logits [T, E]."""
-        T = logits.shape[0]
-        ids = torch.empty((T, self.topk), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((T, self.topk), dtype=torch.float32, device=logits.device)
-        return sq_moe_route(logits, ids, weights, self.router_bias, self.score, self.n_group, self.topk_group,
-                            self.group_top, self.renormalize, self.scale)
-
     def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         """x fp16 [..., K] and router logits [..., E] (fp32 or fp16) -> y fp16 [..., K]."""
         E, F, K = self.up.experts, self.up.N, self.up.K
         if x.dim() < 1 or x.shape[-1] != K or tuple(logits.shape) != tuple(x.shape[:-1]) + (E,):
             raise ValueError(f"x / logits: need [..., {K}] and [..., {E}], got {tuple(x.shape)}, {tuple(logits.shape)}")
+        if x.dtype != torch.float16 or logits.dtype not in (torch.float32, torch.float16):
+            raise ValueError("x: fp16; logits: fp32 or fp16")
         x2, l2 = x.reshape(-1, K), logits.reshape(-1, E)
-        T, P = x2.shape[0], x2.shape[0] * self.topk
-        y = torch.empty(tuple(x.shape), dtype=torch.float16, device=x.device)
+        if x2.stride(1) != 1 or l2.stride(1) != 1:
+            raise ValueError("x / logits: need a unit inner stride")
+        T = x2.shape[0]
+        P = T * self.topk
+        y = torch.empty(x.shape, dtype=torch.float16, device=x.device)
         if T == 0:
             return y
-        ids, weights = self.route(l2)
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=x.device)
-        order = torch.empty(P, dtype=torch.int32, device=x.device)
-        sq_moe_plan(ids, offsets, order)
-        h = torch.empty((P, F), dtype=torch.float16, device=x.device)
-        sq_w4a16_experts(x2, self.up, offsets, order, h, self.topk, self.up_bias, relu=True)
+        # The whole layer is a few tens of microseconds for a few tokens, so the calls below pass
+        # addresses inside one allocation instead of tensors cut from it.
+        up, down, topk = self.up, self.down, self.topk
+        plan_ws = sq_moe_plan_workspace_bytes(P, E)
+        at, end = [], 0
+        for n in (4 * P, 4 * P, 4 * (E + 1), 4 * P, plan_ws, 2 * P * F, 4 * P * K):
+            at.append(end)
+            end += -(-n // 256) * 256
+        buf = torch.empty(end, dtype=torch.uint8, device=x.device)
+        px, pl, prb, pu, pub, pd, pdb, pbuf, py = _ptrs(x2, l2, self.router_bias, up.packed, self.up_bias, down.packed,
+                                                        self.down_bias, buf, y)
+        ids, weights, offsets, order, ws, h, z = (pbuf + a for a in at)
+        st = _stream(None)
+        _check(_L.sq_moe_route(pl, logits.dtype == torch.float16, T, E, l2.stride(0) if T > 1 else E, prb,
+                               _SCORES[self.score], self.n_group, self.topk_group, self.group_top, topk,
+                               self.renormalize, self.scale, ids, weights, st), "sq_moe_route")
+        _check(_L.sq_moe_plan(ids, P, E, offsets, order, ws, plan_ws, st), "sq_moe_plan")
+        _check(_L.sq_w4a16_experts(px, T, x2.stride(0) if T > 1 else K, pu, E, F, K, up.group, up.zero_point, pub, True,
+                                   offsets, order, P, topk, h, False, st), "sq_w4a16_experts")
         # fp32 rows, so that the layer's output is rounded once
-        z = torch.empty((P, K), dtype=torch.float32, device=x.device)
-        sq_w4a16_experts(h, self.down, offsets, order, z, 1, self.down_bias)
-        sq_moe_combine(z, ids, weights, E, y.view(-1, K))
+        _check(_L.sq_w4a16_experts(h, P, F, pd, E, K, F, down.group, down.zero_point, pdb, False, offsets, order, P, 1,
+                                   z, True, st), "sq_w4a16_experts")
+        _check(_L.sq_moe_combine(z, True, ids, weights, T, topk, K, E, py, st), "sq_moe_combine")
         return y
 
     __call__ = forward
