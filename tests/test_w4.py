@@ -167,7 +167,7 @@ def test_quantize(cuda_device, N, K, group, zero, fold):
 def test_quantize_nonfinite_and_extreme(cuda_device, zero):
     import w8a8_int8_linear_channel_b200 as sq
     K, group = 128, 32
-    w = np.zeros((6, K), np.float16)
+    w = np.zeros((8, K), np.float16)
     w[:] = np.linspace(-1, 1, K).astype(np.float16)
     w[0, 5] = np.nan
     w[1, 40] = np.inf
@@ -175,9 +175,11 @@ def test_quantize_nonfinite_and_extreme(cuda_device, zero):
     w[3] = 65504.0
     w[4] = np.float16(2.0**-24)                  # smallest subnormal: the scale rounds to 0 or one step
     w[5, 64:96] = np.nan
-    w4 = sq.new_w4_weight(6, K, group, zero)
+    w[6] = np.arange(K) % 23 * 2.0**-24 - 11 * 2.0**-24      # subnormal scales: -8 has to be clamped to -7
+    w[7] = (np.arange(K) % 31 - 10) * 2.0**-23
+    w4 = sq.new_w4_weight(8, K, group, zero)
     sq.sq_quantize_weight_w4(dev(w), w4)
-    out = torch.empty((6, K), dtype=torch.float16, device="cuda")
+    out = torch.empty((8, K), dtype=torch.float16, device="cuda")
     with np.errstate(invalid="ignore"):
         want = ref.values(*ref.quantize(w, group, zero), group)
     got = host(sq.sq_w4_dequantize(w4, out)).astype(np.float64)

@@ -2,9 +2,9 @@
 // an fp16 weight in groups, packing of codes a caller already has, and the
 // fp16 values of a packed weight.  All three are bound by HBM when they are
 // written so that nothing but the eight values of a packed word is computed
-// per thread: a warp takes two channels, 16 lanes each, lane l the k = 8 l ..
-// 8 l + 7 of a tile (one 16-byte load or store, one packed word), and walks
-// along K with the next tile's load in flight.
+// per thread: a warp takes two channels (the quantizer four), lane l the k =
+// 8 l .. 8 l + 7 of a tile (one 16-byte load or store, one packed word), and
+// walks along K with the next tile's load in flight.
 #include "sq_w4.cuh"
 
 namespace sq {
@@ -17,13 +17,8 @@ constexpr int kRowsPerBlock = 2 * kWarps;
 // Byte offset in a record of the word with k = 8 l .. 8 l + 7 of channel r.
 __device__ __forceinline__ int word_offset(int r, int l) { return r * 64 + (((l & 3) ^ ((r >> 1) & 3)) << 4) + 4 * (l >> 2); }
 
-// Element 2 i in bits 4 i .., element 2 i + 1 sixteen bits higher; c[] < 16.
-__device__ __forceinline__ uint32_t pack_word(const uint32_t (&c)[8]) {
-  uint32_t v = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v |= c[2 * i] << (4 * i) | c[2 * i + 1] << (16 + 4 * i);
-  return v;
-}
+// Element 2 i of a word lies in bits 4 i .., element 2 i + 1 sixteen bits higher.
+__host__ __device__ constexpr int nibble_shift(int e) { return 4 * (e >> 1) + 16 * (e & 1); }
 
 // The tiles [t0, t1) of K that this block's row of the grid takes.
 struct Span {
@@ -52,43 +47,59 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
-// Codes clamp(rint(v / s) + z, lo, hi) (lo, hi and z are integers, so clamping
-// first is the same), division exact as IEEE's, ties to
-// even; a NaN and every value of a group whose scale is 0 or Inf get z.
-// v * (1 / s) is off by at most 2^-22 |v / s| < 2^-17, so it rounds like the
-// quotient unless it lies that close to a half; only then is the division done
-// (about one weight in ten thousand).
-__device__ __forceinline__ void codes_of(const float (&v)[8], float s, float z, float lo, float hi, uint32_t (&c)[8]) {
-  if (!(s > 0.0f) || isinf(s)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = static_cast<uint32_t>(z);
-    return;
-  }
-  const float inv = __frcp_rn(s);
-  // Adding 1.5 * 2^23 rounds to an integer (ties to even) and leaves its low
-  // bits in the mantissa; rintf would go through the slow conversion pipe.
-  constexpr float kMagic = 12582912.0f;
-  const float top = __fadd_rn(hi, -z), bottom = __fadd_rn(lo, -z);
-  float d[8], far = 1.0f;  // the smallest distance of a quotient's fraction from a half
+constexpr float kMagic = 12582912.0f;         // 1.5 * 2^23: a sum with it is an integer in the low mantissa bits
+constexpr uint32_t kMagicBits = 0x4B400000u;
+
+__device__ __forceinline__ float rcp_approx(float s) {
+  float r;  // off by at most one step
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
+
+// The word of the codes clamp(rint(v / s) + z, lo, 15), the quotient as IEEE
+// division gives it, ties to even; a NaN and every value of a group whose
+// scale is 0 or Inf get z.
+// t = v * inv is off by at most 2^-22 t; one correction by the remainder v - t s
+// leaves 2^-44 t before its own rounding.  A quotient of k + 1/2 exactly (one
+// weight in a few hundred: v has 11 bits, s 8) is an fp32 number and so comes out exactly, and any
+// other is at least 2^-12 away from a half: both round as the quotient does.
+// What is left to a slow path is a code out of range (clamped, or a NaN).
+template <bool ZERO>
+__device__ __forceinline__ uint32_t codes_of(const float (&v)[8], float s, float z) {
+  const float inv = rcp_approx(s);
+  // The sum's bits are kMagicBits + code.  z = 8 is even, so adding it with the
+  // magic number leaves ties to even what they are; an odd zero point is added
+  // to the integer instead.
+  const float base = ZERO ? kMagic : kMagic + 8.0f;
+  const uint32_t off = ZERO ? kMagicBits - static_cast<uint32_t>(z) : 0u;
+  uint32_t word = ZERO ? 0u : 0u - kMagicBits * 0x11111111u, range = ZERO ? 0u : kMagicBits;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float t = fminf(fmaxf(__fmul_rn(v[i], inv), bottom), top);
-    d[i] = __fadd_rn(t, kMagic);
-    far = fminf(far, fabsf(__fadd_rn(fabsf(__fadd_rn(t, -__fadd_rn(d[i], -kMagic))), -0.5f)));
+    float t = __fmul_rn(v[i], inv);
+    t = __fmaf_rn(__fmaf_rn(-t, s, v[i]), inv, t);
+    const uint32_t c = __float_as_uint(__fadd_rn(t, base)) - off;
+    range |= c;
+    word += c << nibble_shift(i);
   }
-  // (a NaN lost its sign to the clamp; an inv of Inf, from a subnormal scale, makes NaN and clamped values)
-  bool unsure = !(far > 0x1p-12f) || isinf(inv);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) unsure |= isnan(v[i]);
-  if (unsure) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      d[i] = __fadd_rn(isnan(v[i]) ? 0.0f : fminf(fmaxf(__fdiv_rn(v[i], s), bottom), top), kMagic);
-  }
+  // (a scale below fp16's normal range is so coarse that -8 can come up, which
+  // is in range but clamped)
+  if ((ZERO ? range : range - kMagicBits) < 16u && s >= (ZERO ? 0x1p-24f : 0x1p-14f)) return word;
   const uint32_t zi = static_cast<uint32_t>(z);
+  if (!(s > 0.0f) || isinf(s)) return zi * 0x11111111u;
+  word = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = (__float_as_uint(d[i]) + zi) & 15u;
+  for (int i = 0; i < 8; ++i) {
+    const float q = isnan(v[i]) ? 0.0f : rintf(__fdiv_rn(v[i], s));
+    const float c = fminf(fmaxf(__fadd_rn(q, z), ZERO ? 0.0f : 1.0f), 15.0f);
+    word |= static_cast<uint32_t>(c) << nibble_shift(i);
+  }
+  return word;
 }
+
+// The quantizer is bound by instructions, so a lane takes two words (k = 8 l ..
+// and 64 + 8 l ..) and a warp four channels: what a group costs is shared by
+// more weights.
+constexpr int kQuantRows = 4 * kWarps;
 
 template <int G, bool ZERO>
 __global__ void __launch_bounds__(kWarps * 32)
@@ -96,66 +107,98 @@ __global__ void __launch_bounds__(kWarps * 32)
                   int64_t N, int64_t K, int KT) {
   constexpr int NG = kW4K / G;
   constexpr int REC = w4_record_bytes(G, ZERO);
-  const int l = threadIdx.x & 15;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock + (threadIdx.x >> 4);
+  constexpr int LANES = G >= 64 ? 8 : 4;  // lanes of a group in each half of the tile
+  const int l = threadIdx.x & 7;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * kQuantRows + (threadIdx.x >> 3);
   const int r = static_cast<int>(n & (kW4Rows - 1));
   const Span sp = k_span(KT);
   griddep_wait();
   uint8_t* rec = out + ((n >> 7) * KT + sp.t0) * REC;
-  const __half* row = src + n * K + 8 * l;
-  auto load = [&](int kt) {
-    const int64_t k = static_cast<int64_t>(kt) * kW4K;
-    return kt < sp.t1 && n < N && k + 8 * l < K ? ld_stream(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0, 0, 0, 0);
+  const int k0 = sp.t0 * kW4K + 8 * l;
+  const __half* row = src + n * K + k0;
+  const float* frow = fold ? fold + k0 : nullptr;
+  // k of this lane still to come: none for a channel past N
+  int left = n < N ? static_cast<int>(K) - k0 : 0;
+  auto load = [&](int k) {
+    return left > k ? ld_stream(reinterpret_cast<const uint4*>(row + k)) : make_uint4(0, 0, 0, 0);
   };
-  uint4 next = load(sp.t0);
-  for (int kt = sp.t0; kt < sp.t1; ++kt, rec += REC) {
-    const uint4 raw = next;
-    next = load(kt + 1);
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(reinterpret_cast<const __half2*>(&raw)[i]);
-      v[2 * i] = f.x, v[2 * i + 1] = f.y;
-    }
+  uint4 next[2] = {load(0), load(64)};
+  const int word_at = word_offset(r, l);
+  for (int kt = sp.t0; kt < sp.t1; ++kt) {
+    uint4 raw[2] = {next[0], next[1]};
+    next[0] = kt + 1 < sp.t1 ? load(kW4K) : make_uint4(0, 0, 0, 0);
+    next[1] = kt + 1 < sp.t1 ? load(kW4K + 64) : make_uint4(0, 0, 0, 0);
+    __half2* h[2] = {reinterpret_cast<__half2*>(&raw[0]), reinterpret_cast<__half2*>(&raw[1])};
     if (fold) {
-      const int64_t k = static_cast<int64_t>(kt) * kW4K + 8 * l;
-      if (k < K) {
-        // the folded weight is an fp16 tensor, as in the INT8 quantizer
-        const float4 f0 = *reinterpret_cast<const float4*>(fold + k), f1 = *reinterpret_cast<const float4*>(fold + k + 4);
-        const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+      // the folded weight is an fp16 tensor, as in the INT8 quantizer
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __half2float(__float2half_rn(__fmul_rn(v[i], f[i])));
+      for (int j = 0; j < 2; ++j)
+        if (left > 64 * j) {
+          const float4 f0 = *reinterpret_cast<const float4*>(frow + 64 * j), f1 = *reinterpret_cast<const float4*>(frow + 64 * j + 4);
+          const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 w = __half22float2(h[j][i]);
+            h[j][i] = __floats2half2_rn(__fmul_rn(w.x, f[2 * i]), __fmul_rn(w.y, f[2 * i + 1]));
+          }
+        }
+      frow += kW4K;
+    }
+    // ranges, in fp16 (exact; the maximum drops a NaN, so it never sets a range)
+    float hi[2], lo[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const __half2 zero = __float2half2_rn(0.0f);
+      __half2 a = zero, b = zero;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a = __hmax2(a, ZERO ? h[j][i] : __habs2(h[j][i]));
+        if (ZERO) b = __hmax2(b, __hneg2(h[j][i]));
       }
+      hi[j] = __half2float(__hmax(__low2half(a), __high2half(a)));
+      lo[j] = __half2float(__hmax(__low2half(b), __high2half(b)));
     }
-    float s, z;
-    uint32_t c[8];
-    if (ZERO) {
-      // fmaxf drops a NaN, so it never sets a range
-      float hi = 0.0f, lo = 0.0f;
+    if (G == 128) {
+      hi[0] = fmaxf(hi[0], hi[1]);
+      lo[0] = fmaxf(lo[0], lo[1]);
+    }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) hi = fmaxf(hi, v[i]), lo = fmaxf(lo, -v[i]);
-      hi = group_max<G / 8>(hi);
-      lo = group_max<G / 8>(lo);
-      // 7 significant bits: |q - z| <= 15 takes 4, so (q - z) * s fits fp16's 11
-      s = __half2float(__float2half_rn(round_bits(__fdiv_rn(__fadd_rn(hi, lo), 15.0f), 7)));
-      z = (s > 0.0f && !isinf(s)) ? fminf(rintf(__fdiv_rn(lo, s)), 15.0f) : 0.0f;
-      codes_of(v, s, z, 0.0f, 15.0f, c);
-    } else {
-      float m = 0.0f;
+    for (int j = 0; j < (G == 128 ? 1 : 2); ++j) {
+      hi[j] = group_max<LANES>(hi[j]);
+      if (ZERO) lo[j] = group_max<LANES>(lo[j]);
+    }
+    float s = 0.0f, z = 8.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-      m = group_max<G / 8>(m);
-      // 8 significant bits: |q| <= 7 takes 3, so q * s fits fp16's 11
-      s = __half2float(__float2half_rn(round_bits(__fdiv_rn(m, 7.0f), 8)));
-      z = 8.0f;
-      codes_of(v, s, z, 1.0f, 15.0f, c);
+    for (int j = 0; j < 2; ++j) {
+      if (j == 0 || G != 128) {
+        if (ZERO) {
+          // 7 significant bits: |q - z| <= 15 takes 4, so (q - z) * s fits fp16's 11
+          s = __half2float(__float2half_rn(round_bits(__fdiv_rn(__fadd_rn(hi[j], lo[j]), 15.0f), 7)));
+          z = (s > 0.0f && !isinf(s)) ? fminf(rintf(__fdiv_rn(lo[j], s)), 15.0f) : 0.0f;
+        } else {
+          // 8 significant bits: |q| <= 7 takes 3, so q * s fits fp16's 11.  The
+          // maximum has 11 bits, seven times the middle of two 8-bit numbers has
+          // 12: a seventh is never halfway, nor nearer to it than 2^-14, and the
+          // product rounds like it.
+          s = __half2float(__float2half_rn(round_bits(__fmul_rn(hi[j], 1.0f / 7.0f), 8)));
+        }
+        const int g = G == 32 ? 2 * j + (l >> 2) : G == 64 ? j : 0;
+        if ((l & (LANES - 1)) == 0) {
+          *reinterpret_cast<__half*>(rec + kW4CodeBytes + (r * NG + g) * 2) = __float2half_rn(s);
+          if (ZERO) rec[kW4CodeBytes + kW4Rows * NG * 2 + r * NG + g] = static_cast<uint8_t>(z);
+        }
+      }
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(h[j][i]);
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+      }
+      *reinterpret_cast<uint32_t*>(rec + word_at + 8 * j) = codes_of<ZERO>(v, s, z);
     }
-    *reinterpret_cast<uint32_t*>(rec + word_offset(r, l)) = pack_word(c);
-    if ((l & (G / 8 - 1)) == 0) {
-      const int g = l / (G / 8);
-      *reinterpret_cast<__half*>(rec + kW4CodeBytes + (r * NG + g) * 2) = __float2half_rn(s);
-      if (ZERO) rec[kW4CodeBytes + kW4Rows * NG * 2 + r * NG + g] = static_cast<uint8_t>(z);
-    }
+    rec += REC;
+    row += kW4K;
+    left -= kW4K;
   }
 }
 
@@ -181,15 +224,14 @@ __global__ void __launch_bounds__(kWarps * 32)
       s = scales[n * groups + g];
       if (ZERO) z = zeros[n * groups + g] & 15u;
     }
-    uint32_t c[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = z;
+    uint32_t word = z * 0x11111111u;
     if (n < N && k < K) {
       const uint2 raw = *reinterpret_cast<const uint2*>(codes + n * K + k);
+      word = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = (raw.x >> (8 * i)) & 15u, c[4 + i] = (raw.y >> (8 * i)) & 15u;
+      for (int i = 0; i < 8; ++i) word |= (((i < 4 ? raw.x : raw.y) >> (8 * (i & 3))) & 15u) << nibble_shift(i);
     }
-    *reinterpret_cast<uint32_t*>(rec + word_offset(r, l)) = pack_word(c);
+    *reinterpret_cast<uint32_t*>(rec + word_offset(r, l)) = word;
     if ((l & (G / 8 - 1)) == 0) {
       const int gi = l / (G / 8);
       *reinterpret_cast<__half*>(rec + kW4CodeBytes + (r * NG + gi) * 2) = s;
@@ -244,10 +286,10 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-// Blocks of 16 channels; K is split until about 32 warps per SM exist (a
+// Blocks of per_block channels; K is split until about 32 warps per SM exist (a
 // narrow weight would otherwise walk K in too few warps).
-dim3 grid_for(int64_t rows, int64_t kt, const Ctx& c) {
-  const int64_t x = (rows + kRowsPerBlock - 1) / kRowsPerBlock;
+dim3 grid_for(int64_t rows, int per_block, int64_t kt, const Ctx& c) {
+  const int64_t x = (rows + per_block - 1) / per_block;
   int64_t y = (static_cast<int64_t>(c.num_sms) * 4 + x - 1) / x;
   if (y > kt) y = kt;
   return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
@@ -269,7 +311,7 @@ dim3 grid_for(int64_t rows, int64_t kt, const Ctx& c) {
 
 cudaError_t launch_w4_pack(const uint8_t* codes, const __half* scales, const uint8_t* zeros, const W4Weight& w,
                            const Ctx& c) {
-  const dim3 grid = grid_for(w.nt() * kW4Rows, w.kt(), c);
+  const dim3 grid = grid_for(w.nt() * kW4Rows, kRowsPerBlock, w.kt(), c);
 #define SQ_CALL(G, Z)                                                                                              \
   launch_pdl(k_w4_pack<G, Z>, grid, dim3(kWarps * 32), 0, c.stream, codes, scales, zeros, w.data, w.N, w.K, w.kt())
   SQ_W4_DISPATCH(w, SQ_CALL);
@@ -277,7 +319,7 @@ cudaError_t launch_w4_pack(const uint8_t* codes, const __half* scales, const uin
 }
 
 cudaError_t launch_w4_quantize(const __half* src, const float* s, const W4Weight& w, const Ctx& c) {
-  const dim3 grid = grid_for(w.nt() * kW4Rows, w.kt(), c);
+  const dim3 grid = grid_for(w.nt() * kW4Rows, kQuantRows, w.kt(), c);
 #define SQ_CALL(G, Z) \
   launch_pdl(k_w4_quantize<G, Z>, grid, dim3(kWarps * 32), 0, c.stream, src, s, w.data, w.N, w.K, w.kt())
   SQ_W4_DISPATCH(w, SQ_CALL);
@@ -285,7 +327,7 @@ cudaError_t launch_w4_quantize(const __half* src, const float* s, const W4Weight
 }
 
 cudaError_t launch_w4_dequantize(const W4Weight& w, __half* out, const Ctx& c) {
-  const dim3 grid = grid_for(w.N, w.kt(), c);
+  const dim3 grid = grid_for(w.N, kRowsPerBlock, w.kt(), c);
 #define SQ_CALL(G, Z)                                                                                           \
   launch_pdl(k_w4_dequantize<G, Z>, grid, dim3(kWarps * 32), 0, c.stream, static_cast<const uint8_t*>(w.data),   \
              out, w.N, w.K, w.kt())
