@@ -48,7 +48,8 @@ struct Layout {
   static constexpr int REC = w4_record_bytes(G, ZERO);
   static constexpr int X = REC;
   static constexpr int STAGE = REC + BT * kTokenPitch;
-  static constexpr int STAGES = NB == 1 ? 6 : 4;  // even: a K group keeps to its half of the stages
+  // even (a K group keeps to its half of the stages), and such that three CTAs fit an SM (two of 16 tokens)
+  static constexpr int STAGES = NB == 1 && 6 * STAGE <= 67 * 1024 ? 6 : 4;
   // sums of every slice and K group for the channels this CTA finishes:
   // fp32 [slices * kKGroups][channels per CTA][BT]
   static constexpr int RED = STAGES * STAGE;
@@ -137,7 +138,7 @@ __device__ __forceinline__ void consume(uint32_t stage, const uint8_t* rec, int 
 
 template <int NB, int G, bool ZERO>
 __global__ void __launch_bounds__(kThreads)
-    k_w4_stream(const W4Product p, int slices, int blocks, int KT, uint32_t* status, uint64_t budget) {
+    k_w4_stream(const W4Product p, int slices, int KT, int nt, uint32_t share_inv, uint32_t* status, uint64_t budget) {
   using L = Layout<NB, G, ZERO>;
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -147,9 +148,9 @@ __global__ void __launch_bounds__(kThreads)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // consecutive clusters take the token blocks of one weight tile (the tile
   // comes from L2 after the first)
-  const int slice = blockIdx.x % slices;
-  const int block = blockIdx.x / slices % blocks;
-  const int tile = blockIdx.x / slices / blocks;
+  const int slice = static_cast<int>(cluster_ctarank());
+  const int block = static_cast<int>(cluster_id_x());
+  const int tile = static_cast<int>(blockIdx.y);
   const uint32_t full = sbase + L::BARS, empty = full + 8 * L::STAGES;
 
   if (tid == 0) {
@@ -189,15 +190,16 @@ __global__ void __launch_bounds__(kThreads)
     if (expert < 0) return;  // the same for every CTA of the cluster
   }
 
-  const int kt0 = static_cast<int>(static_cast<int64_t>(KT) * slice / slices);
-  const int n = static_cast<int>(static_cast<int64_t>(KT) * (slice + 1) / slices) - kt0;
+  const int each = KT / slices, more = KT - each * slices;  // K tiles per slice, slices with one more
+  const int kt0 = each * slice + min(slice, more);
+  const int n = each + (slice < more ? 1 : 0);
   const int tail = static_cast<int>(p.w.K & (kW4K - 1));  // k of the last tile when it is short
   const int share = (kW4Rows + slices - 1) / slices;       // channels each CTA of the cluster finishes
 
   int issued = 0;  // stages the producer filled
   if (warp == kConsumers) {
     // ---- producer: one record and the block's token rows per stage
-    const uint8_t* rec = p.w.data + ((static_cast<int64_t>(expert) * p.w.nt() + tile) * KT + kt0) * L::REC;
+    const uint8_t* rec = p.w.data + ((static_cast<int64_t>(expert) * nt + tile) * KT + kt0) * L::REC;
     const __half* xrow = nullptr;
     if (lane < count && rows[lane] >= 0)
       xrow = p.x + static_cast<int64_t>(rows[lane] / p.div) * p.ldx + static_cast<int64_t>(kt0) * kW4K;
@@ -235,13 +237,6 @@ __global__ void __launch_bounds__(kThreads)
     const int kg = warp / kRowGroups;
     const int r0 = (warp % kRowGroups) * 32 + g;
     if (slices > 1) cluster_arrive();
-    // token slots without a row are zero in every stage, once
-    for (int tk = warp; tk < L::BT; tk += kConsumers)
-      if (rows[tk] < 0)
-        for (int i = lane; i < L::STAGES * 16; i += 32)
-          *reinterpret_cast<uint4*>(smem + (i >> 4) * L::STAGE + L::X + tk * kTokenPitch + (i & 15) * 16) =
-              make_uint4(0, 0, 0, 0);
-    named_bar_sync(1, kConsumers * 32);
     float acc[2][NB][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -273,7 +268,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = r0 + 16 * m + 8 * h;
-        const int owner = r / share;
+        const int owner = static_cast<int>(r * share_inv >> 16);  // r / share
         uint32_t at = sbase + L::RED + ((src + r - owner * share) * L::BT + 2 * t) * 4;
         if (slices > 1) at = mapa_shared(at, owner);
 #pragma unroll
@@ -302,19 +297,22 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t n0 = static_cast<int64_t>(tile) * kW4Rows + slice * share;
   const int64_t left = min(p.w.N - n0, static_cast<int64_t>(kW4Rows - slice * share));
   const int width = static_cast<int>(left < share ? left : share);
-  for (int i = tid; i < width * count; i += kThreads) {
-    const int tk = i / width, r = i - tk * width;
-    if (rows[tk] < 0) continue;
-    float v = 0.0f;
+  const int sums = slices * kKGroups;
+  for (int tk = warp; tk < count; tk += kConsumers + 1) {
+    const int row = rows[tk];
+    if (row < 0) continue;
+    for (int r = lane; r < width; r += 32) {
+      float v = 0.0f;
 #pragma unroll 4
-    for (int c = 0; c < slices * kKGroups; ++c) v = __fadd_rn(v, red[(c * share + r) * L::BT + tk]);
-    if (p.bias) v = __fadd_rn(v, __half2float(p.bias[static_cast<int64_t>(expert) * p.w.N + n0 + r]));
-    if (p.relu) v = v > 0.0f ? v : 0.0f;
-    const int64_t o = static_cast<int64_t>(rows[tk]) * p.w.N + n0 + r;
-    if (p.y)
-      p.y[o] = __float2half_rn(v);
-    else
-      p.y32[o] = v;
+      for (int c = 0; c < sums; ++c) v = __fadd_rn(v, red[(c * share + r) * L::BT + tk]);
+      if (p.bias) v = __fadd_rn(v, __half2float(p.bias[static_cast<int64_t>(expert) * p.w.N + n0 + r]));
+      if (p.relu) v = v > 0.0f ? v : 0.0f;
+      const int64_t o = static_cast<int64_t>(row) * p.w.N + n0 + r;
+      if (p.y)
+        p.y[o] = __float2half_rn(v);
+      else
+        p.y32[o] = v;
+    }
   }
 }
 
@@ -329,9 +327,11 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   const int64_t nt = p.w.nt(), kt = p.w.kt();
   const int64_t blocks = w4_blocks(p, L::BT);
   const int slices = w4_slices(nt * blocks, kt, static_cast<int64_t>(c.num_sms) * per_sm, 6);
+  // ceil(2^16 / share): r * share_inv >> 16 is r / share for every channel r < 128
+  const uint32_t share = (kW4Rows + slices - 1) / slices, share_inv = (65536 + share - 1) / share;
   cudaLaunchConfig_t cfg = {};
-  if (nt * blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3(static_cast<unsigned>(nt * blocks * slices));
+  if (nt > 65535 || blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * slices), static_cast<unsigned>(nt));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = L::BYTES;
   cfg.stream = c.stream;
@@ -344,7 +344,7 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, slices, static_cast<int>(blocks), static_cast<int>(kt), c.status, c.budget_ns);
+  return cudaLaunchKernelEx(&cfg, kernel, p, slices, static_cast<int>(kt), static_cast<int>(nt), share_inv, c.status, c.budget_ns);
 }
 
 template <int NB>
