@@ -83,7 +83,7 @@ struct W4Product {
   int div;
 };
 cudaError_t launch_w4_product(const W4Product& p, const Ctx& c);
-cudaError_t launch_w4_stream(const W4Product& p, const Ctx& c, int64_t tokens);  // few tokens per weight tile
+cudaError_t launch_w4_stream(const W4Product& p, const Ctx& c);                  // up to eight tokens per weight tile
 cudaError_t launch_w4_gemm(const W4Product& p, const Ctx& c, int64_t tokens);    // more
 // Blocks of bt tokens: exactly, or for experts the most that any routing of
 // the pairs can need (CTAs of blocks that do not exist leave at once).
