@@ -9,7 +9,7 @@
 // 8-column one (fp32 accumulators); a group's sum is multiplied by its scale
 // once, in fp32, so no weight is ever rounded.
 //
-// Every warp is a stream of its own: it owns 32 channels and every other K
+// Every warp is a stream of its own: it owns 32 channels and every fourth K
 // tile of its CTA's slice, loads a tile's codes (2 KB, contiguous) and scales
 // straight into registers while it computes on the tile before, and shares
 // nothing with other warps until the end.  The arithmetic is what bounds this kernel (about 185 warp
@@ -18,8 +18,8 @@
 // same arithmetic behind a ring of bulk copies in shared memory, 100 more
 // instructions per tile went into barriers and the producer.
 //
-// A CTA owns one 128-channel tile and a slice of K; the CTAs of a cluster own
-// the slices of one tile.  At the end every warp pushes its sums to the CTA of
+// A CTA owns half a 128-channel tile and a slice of K; the CTAs of a cluster own
+// the slices of one half.  At the end every warp pushes its sums to the CTA of
 // the cluster that finishes those channels (distributed shared memory), which
 // adds them in a fixed order: no atomics, no workspace, the same bits on every
 // run.
@@ -28,9 +28,8 @@
 namespace sq {
 namespace {
 
-constexpr int kRowGroups = 4;  // warps along the channels, 32 each
-constexpr int kKGroups = 2;    // warps along K: even and odd tiles
-constexpr int kThreads = kRowGroups * kKGroups * 32;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
 constexpr int kTokens = 8;
 constexpr int kMaxSlices = 8;  // portable cluster size
 
@@ -92,18 +91,27 @@ struct Ring {
   }
 };
 
-// One K tile: x points at this lane's token and k (8 t of the tile), NULL when
-// the token slot is empty (its column then comes out 0); klen is how many of the tile's k exist.
-template <int G, bool ZERO>
-__device__ __forceinline__ void consume(const uint8_t* stage, int lane, const __half* x, int klen, float (&acc)[2][4]) {
+// The k of a tile's four steps that a lane holds of its token: 32 q + 8 t ...
+// With TAIL only klen of the tile's k exist; a step past them reads the row's
+// first k of the tile instead (some address that exists).
+template <bool TAIL>
+__device__ __forceinline__ uint4 ld_step(const __half* x, int q, int t, int klen) {
+  return ld_x(!TAIL || 32 * q + 8 * t < klen ? x + 32 * q : x - 8 * t);
+}
+
+// One K tile.  xv holds this lane's token (a lane whose token slot is empty has
+// some other token: its column goes nowhere); every step's registers are
+// loaded again, for the next tile (at xnext), as soon as they have been used.
+template <int G, bool ZERO, bool TAIL, bool NEXT_TAIL>
+__device__ __forceinline__ void consume(const uint8_t* stage, int lane, uint4 (&xv)[4], const __half* xnext, int klen,
+                                        float (&acc)[2][4]) {
   using R = Ring<G, ZERO>;
   constexpr int NG = R::NG;
   const int g = lane >> 2, t = lane & 3;
-  uint4 xv[4];
+  if (TAIL) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    xv[q] = make_uint4(0, 0, 0, 0);
-    if (x && 32 * q + 8 * t < klen) xv[q] = ld_x(x + 32 * q);
+    for (int q = 0; q < 4; ++q)
+      if (32 * q + 8 * t >= klen) xv[q] = make_uint4(0, 0, 0, 0);
   }
   uint4 codes[4];
 #pragma unroll
@@ -138,6 +146,7 @@ __device__ __forceinline__ void consume(const uint8_t* stage, int lane, const __
           mma_f16(part[m], a0[0], a1[0], a0[1], a1[1], xv[q].x, xv[q].y);
         mma_f16(part[m], a0[2], a1[2], a0[3], a1[3], xv[q].z, xv[q].w);
       }
+      xv[q] = ld_step<NEXT_TAIL>(xnext, q, t, klen);
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -150,28 +159,31 @@ __device__ __forceinline__ void consume(const uint8_t* stage, int lane, const __
   }
 }
 
-template <int G, bool ZERO>
+// kRowGroups warps along the channels, 32 each, and the others along K.
+template <int kRowGroups, int G, bool ZERO>
 __global__ void __launch_bounds__(kThreads, 3)
     k_w4_stream(const W4Product p, int slices, int KT, int nt, uint32_t share_inv) {
+  constexpr int kKGroups = kWarps / kRowGroups;
+  constexpr int kRows = kRowGroups * 32, kParts = kW4Rows / kRows;  // channels per CTA, CTAs per weight tile
   using R = Ring<G, ZERO>;
   constexpr int REC = w4_record_bytes(G, ZERO);
   // sums of every slice and K group for the channels this CTA finishes:
   // [slices * kKGroups][channels per CTA][kTokens]
   extern __shared__ __align__(128) uint8_t smem[];  // every warp's ring
-  __shared__ __align__(16) float red[kKGroups * (kW4Rows + kMaxSlices) * kTokens];
+  __shared__ __align__(16) float red[kKGroups * (kRows + kMaxSlices) * kTokens];
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int slice = static_cast<int>(cluster_ctarank());
-  const int block = static_cast<int>(cluster_id_x());
-  const int tile = static_cast<int>(blockIdx.y);
+  const int tile = static_cast<int>(blockIdx.y) / kParts, part0 = static_cast<int>(blockIdx.y) % kParts * kRows;
   const int g = lane >> 2, t = lane & 3;
-  const int kg = warp / kRowGroups, r0 = (warp % kRowGroups) * 32 + g;
+  const int kg = warp / kRowGroups, r0 = (warp % kRowGroups) * 32 + g;  // channel of this CTA's
   const int each = KT / slices, more = KT - each * slices;  // K tiles per slice, slices with one more
   const int kt0 = each * slice + min(slice, more);
   const int n = each + (slice < more ? 1 : 0);
   if (slices > 1) cluster_arrive();  // waited for before the pushes: every CTA of the cluster runs by then
   griddep_wait();
 
+  const int block = static_cast<int>(cluster_id_x());
   // this lane's token: slot g of the block
   int expert = 0, count, row = -1;
   if (p.offsets == nullptr) {
@@ -190,7 +202,6 @@ __global__ void __launch_bounds__(kThreads, 3)
       if (pair >= 0 && pair < p.M) row = pair;
     }
   }
-
   float acc[2][4];
 #pragma unroll
   for (int m = 0; m < 2; ++m)
@@ -199,15 +210,16 @@ __global__ void __launch_bounds__(kThreads, 3)
   {
     const uint8_t* rec =
         p.w.data + ((static_cast<int64_t>(expert) * nt + tile) * KT + kt0 + kg) * static_cast<int64_t>(REC);
-    const __half* x = row < 0 ? nullptr
-                              : p.x + static_cast<int64_t>(p.div == 1 ? row : row / p.div) * p.ldx +
-                                    static_cast<int64_t>(kt0 + kg) * kW4K + 8 * t;
-    int left = static_cast<int>(p.w.K) - (kt0 + kg) * kW4K;  // k from this tile on
+    const int some = row < 0 ? 0 : p.div == 1 ? row : row / p.div;
+    const __half* x = p.x + some * p.ldx + static_cast<int64_t>(kt0 + kg) * kW4K + 8 * t;
+    // the CTA's last tile when it is short (its length: tail)
+    const int tail = static_cast<int>(p.w.K) & (kW4K - 1);
+    const int last = tail && kt0 + n == KT ? n - 1 : -1;
     // (the chunk's place is the same for r0, r0 + 8, r0 + 16, r0 + 24)
-    const uint32_t code_at = r0 * 64 + ((t ^ ((r0 >> 1) & 3)) << 4);
+    const uint32_t code_at = (part0 + r0) * 64 + ((t ^ ((r0 >> 1) & 3)) << 4);
     uint8_t* ring = smem + warp * R::WARP;
     const uint32_t ring_at = smem_u32(ring);
-    const int first = (warp % kRowGroups) * 32;
+    const int first = part0 + (warp % kRowGroups) * 32;
 #pragma unroll
     for (int d = 0; d < kDepth - 1; ++d) {
       if (kg + d * kKGroups < n) R::copy(ring_at + d * R::STAGE, rec + d * (kKGroups * REC), first, lane, code_at);
@@ -215,15 +227,25 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     rec += (kDepth - 1) * (kKGroups * REC);
     int now = 0, ahead = (kDepth - 1) * R::STAGE;  // byte offsets of this tile's stage and of the one to fill
+    uint4 xv[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      xv[q] = make_uint4(0, 0, 0, 0);
+      if (kg < n) xv[q] = kg == last ? ld_step<true>(x, q, t, tail) : ld_step<false>(x, q, t, 0);
+    }
     for (int i = kg; i < n; i += kKGroups) {
       cp_async_wait<kDepth - 2>();
       __syncwarp();  // the other lanes' scales have landed too, and the stage to fill has been read
       if (i + (kDepth - 1) * kKGroups < n) R::copy(ring_at + ahead, rec, first, lane, code_at);
       cp_async_commit();
       rec += kKGroups * REC;
-      consume<G, ZERO>(ring + now, lane, x, left, acc);
-      if (x) x += kKGroups * kW4K;
-      left -= kKGroups * kW4K;
+      if (i + kKGroups < n) x += kKGroups * kW4K;  // (the last tile loads itself again)
+      if (i == last)
+        consume<G, ZERO, true, true>(ring + now, lane, xv, x, tail, acc);
+      else if (i + kKGroups == last)
+        consume<G, ZERO, false, true>(ring + now, lane, xv, x, tail, acc);
+      else
+        consume<G, ZERO, false, false>(ring + now, lane, xv, x, 0, acc);
       now = now == (kDepth - 1) * R::STAGE ? 0 : now + R::STAGE;
       ahead = ahead == (kDepth - 1) * R::STAGE ? 0 : ahead + R::STAGE;
     }
@@ -231,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   griddep_launch_dependents();
 
   // push the sums to the CTAs that finish these channels
-  const int share = (kW4Rows + slices - 1) / slices;  // channels each CTA of the cluster finishes
+  const int share = (kRows + slices - 1) / slices;  // channels each CTA of the cluster finishes
   if (slices > 1) cluster_wait();
   const uint32_t src = (slice * kKGroups + kg) * share;
 #pragma unroll
@@ -254,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, 3)
   // Each CTA of the cluster finishes its share of the tile's channels, a warp per token.
   const int out = __shfl_sync(0xffffffffu, row, 4 * warp);
   if (out < 0) return;
-  const int64_t n0 = static_cast<int64_t>(tile) * kW4Rows + slice * share;
-  const int64_t left = min(p.w.N - n0, static_cast<int64_t>(kW4Rows - slice * share));
+  const int64_t n0 = static_cast<int64_t>(tile) * kW4Rows + part0 + slice * share;
+  const int64_t left = min(p.w.N - n0, static_cast<int64_t>(kRows - slice * share));
   const int width = static_cast<int>(left < share ? left : share);
   const int sums = slices * kKGroups;
   for (int r = lane; r < width; r += 32) {
@@ -272,22 +294,35 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
 }
 
-template <int G, bool ZERO>
+// Slices of K (the cluster size): as many as give every SM one CTA, a K tile
+// per warp at least.  More would share SMs and pay for larger clusters: 4096 x 4096 at
+// one token takes 6.6 / 5.0 / 6.2 us with 1 / 2 / 4 slices, 4096 x 16384 19.5 /
+// 12.0 / 12.4, 16384 x 4096 (256 CTAs already) 12.0 / 14.0 / 17.2.
+int pick_slices(int64_t ctas, int64_t kt, int k_groups, int num_sms) {
+  int64_t s = num_sms / ctas;
+  if (s > kt / k_groups) s = kt / k_groups;
+  return s < 1 ? 1 : s > kMaxSlices ? kMaxSlices : static_cast<int>(s);
+}
+
+template <int kRowGroups, int G, bool ZERO>
 cudaError_t launch(const W4Product& p, const Ctx& c) {
-  auto kernel = k_w4_stream<G, ZERO>;
-  constexpr size_t smem = kRowGroups * kKGroups * Ring<G, ZERO>::WARP;
+  auto kernel = k_w4_stream<kRowGroups, G, ZERO>;
+  constexpr int kKGroups = kWarps / kRowGroups, kRows = kRowGroups * 32;
+  constexpr size_t smem = kWarps * Ring<G, ZERO>::WARP;
   static KernelSetup setup;
-  int per_sm = 0;
+  int per_sm;
   const cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(kernel), kThreads, smem, c.device, &per_sm);
   if (e != cudaSuccess) return e;
   const int64_t nt = p.w.nt(), kt = p.w.kt();
-  const int64_t blocks = w4_blocks(p, kTokens);
-  const int slices = w4_slices(nt * blocks, kt, static_cast<int64_t>(c.num_sms) * per_sm, 6);
-  // ceil(2^16 / share): r * share_inv >> 16 is r / share for every channel r < 128
-  const uint32_t share = (kW4Rows + slices - 1) / slices, share_inv = (65536 + share - 1) / share;
-  if (nt > 65535 || blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const int64_t blocks = w4_blocks(p, kTokens), units = (p.w.N + kRows - 1) / kRows;
+  // (experts: about a block each, if there are that many pairs)
+  const int64_t likely = !p.offsets ? blocks : p.M < p.E ? p.M : p.E;
+  const int slices = pick_slices(units * likely, kt, kKGroups, c.num_sms);
+  // ceil(2^16 / share): r * share_inv >> 16 is r / share for every channel r of the CTA
+  const uint32_t share = (kRows + slices - 1) / slices, share_inv = (65536 + share - 1) / share;
+  if (units > 65535 || blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks * slices), static_cast<unsigned>(nt));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * slices), static_cast<unsigned>(units));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
@@ -303,17 +338,26 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   return cudaLaunchKernelEx(&cfg, kernel, p, slices, static_cast<int>(kt), static_cast<int>(nt), share_inv);
 }
 
+template <int kRowGroups>
+cudaError_t launch_g(const W4Product& p, const Ctx& c) {
+  if (p.w.zero) {
+    if (p.w.group == 32) return launch<kRowGroups, 32, true>(p, c);
+    if (p.w.group == 64) return launch<kRowGroups, 64, true>(p, c);
+    return launch<kRowGroups, 128, true>(p, c);
+  }
+  if (p.w.group == 32) return launch<kRowGroups, 32, false>(p, c);
+  if (p.w.group == 64) return launch<kRowGroups, 64, false>(p, c);
+  return launch<kRowGroups, 128, false>(p, c);
+}
+
 }  // namespace
 
 cudaError_t launch_w4_stream(const W4Product& p, const Ctx& c) {
-  if (p.w.zero) {
-    if (p.w.group == 32) return launch<32, true>(p, c);
-    if (p.w.group == 64) return launch<64, true>(p, c);
-    return launch<128, true>(p, c);
-  }
-  if (p.w.group == 32) return launch<32, false>(p, c);
-  if (p.w.group == 64) return launch<64, false>(p, c);
-  return launch<128, false>(p, c);
+  // Two warps along the channels and four along K where CTAs are few (4096 x
+  // 4096 at one token 5.0 us against 6.9), four and two where they fill the GPU several
+  // times over (an expert layer of 32 tokens 164 us against 172).
+  const int64_t likely = !p.offsets ? w4_blocks(p, kTokens) : p.M < p.E ? p.M : p.E;
+  return p.w.nt() * likely >= 3 * c.num_sms ? launch_g<4>(p, c) : launch_g<2>(p, c);
 }
 
 int64_t w4_blocks(const W4Product& p, int bt) {
