@@ -132,7 +132,7 @@ struct Layout {
   static constexpr int X = 0;
   static constexpr int R = X + (XS * XSTAGE > RED_BYTES || RT == 2 ? XS * XSTAGE : (RED_BYTES + 1023) / 1024 * 1024);
   static constexpr int BARS = R + RS * RT * REC;
-  static constexpr int NBARS = 2 * XS + 2 * RS + 2 * AS + 1;
+  static constexpr int NBARS = 2 * XS + 2 * RS + AS + 1;
   static constexpr int XROW = BARS + (NBARS * 8 + 15) / 16 * 16;  // int32 [BT]: x row of every token, -1 none
   static constexpr int YROW = XROW + BT * 4;                      // int32 [BT]: y row, -1 none
   static constexpr int MISC = YROW + BT * 4;                      // abort, TMEM address, expert, count
@@ -169,21 +169,19 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   const int slice = blockIdx.x % slices;
   const int block = blockIdx.x / slices % blocks;
   const int tile = blockIdx.x / slices / blocks * RT;  // first weight tile
-  const uint32_t x_full = sbase + L::BARS, x_empty = x_full + 8 * L::XS;
-  const uint32_t r_full = x_empty + 8 * L::XS, r_empty = r_full + 8 * L::RS;
-  const uint32_t a_full = r_empty + 8 * L::RS, a_empty = a_full + 8 * L::AS;
-  const uint32_t d_full = a_empty + 8 * L::AS;
+  // done: the MMAs of a K tile have run, one barrier per token stage (it frees
+  // the operand buffer too: a buffer's tile is AS <= XS + 1 tiles back)
+  const uint32_t x_full = sbase + L::BARS, done = x_full + 8 * L::XS;
+  const uint32_t r_full = done + 8 * L::XS, r_empty = r_full + 8 * L::RS;
+  const uint32_t a_full = r_empty + 8 * L::RS, d_full = a_full + 8 * L::AS;
 
   if (tid == 0) {
-    for (int s = 0; s < L::XS; ++s) mbar_init(x_full + 8 * s, p.offsets ? L::X_THREADS : 1), mbar_init(x_empty + 8 * s, 1);
+    for (int s = 0; s < L::XS; ++s) mbar_init(x_full + 8 * s, p.offsets ? L::X_THREADS : 1), mbar_init(done + 8 * s, 1);
     for (int s = 0; s < L::RS; ++s) {
       mbar_init(r_full + 8 * s, 1);
       mbar_init(r_empty + 8 * s, RT == 2 ? 8 : 4);
     }
-    for (int s = 0; s < L::AS; ++s) {
-      mbar_init(a_full + 8 * s, RT == 2 ? 8 : 4);
-      mbar_init(a_empty + 8 * s, 1);
-    }
+    for (int s = 0; s < L::AS; ++s) mbar_init(a_full + 8 * s, RT == 2 ? 8 : 4);
     mbar_init(d_full, 1);
     *abort = 0;
     fence_barrier_init();
@@ -236,9 +234,8 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     const int parity = warp >> (RT == 2 ? 3 : 2);
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
-    // stage and buffer counters in steps of two tiles (an `empty` barrier that
-    // nobody has used yet answers parity 1 at once)
-    uint32_t rs = parity, rp = 0, as = parity, ap = 1;
+    // stage and buffer counters in steps of two tiles
+    uint32_t rs = parity, rp = 0, as = parity;
     for (int i = parity; i < n; i += 2) {
       if (!w4_wait_warp(r_full + 8 * rs, rp, budget, status, abort)) break;
       const int rec = L::R + (rs * RT + t) * L::REC;
@@ -254,33 +251,41 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(r_empty + 8 * rs);
-      if (!w4_wait_warp(a_empty + 8 * as, ap, budget, status, abort)) break;
-      tc_fence_after();
       const uint32_t col = tmem + L::A0 + (as * RT + t) * kACols + lanes;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      auto values = [&](int w, uint32_t (&v)[16]) {
         const int j = w / (G / 32);
         const uint32_t lo = 0x64006400u | z[j] | z[j] << 16, hi = 0xD400D400u | z[j] << 4 | z[j] << 20;
-        const uint32_t word[4] = {w == 0 ? c[0].x : w == 1 ? c[0].y : w == 2 ? c[0].z : c[0].w,
-                                  w == 0 ? c[1].x : w == 1 ? c[1].y : w == 2 ? c[1].z : c[1].w,
-                                  w == 0 ? c[2].x : w == 1 ? c[2].y : w == 2 ? c[2].z : c[2].w,
-                                  w == 0 ? c[3].x : w == 1 ? c[3].y : w == 2 ? c[3].z : c[3].w};
-        uint32_t v[16];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t h[4];
-          dequant(word[q], lo, hi, h);
+          dequant(w == 0 ? c[q].x : w == 1 ? c[q].y : w == 2 ? c[q].z : c[q].w, lo, hi, h);
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[4 * q + e] = hmul2(h[e], s2[j]);
         }
-        tmem_st_x16(col + 16 * w, v);
-      }
+      };
+      // Half of the values are made before the buffer is free, so that the MMAs
+      // of the tile before (1070 cycles with 128 tokens and two weight tiles) cover the other half.
+      uint32_t v0[16], v1[16];
+      values(0, v0);
+      values(1, v1);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(v0[e]), "+r"(v1[e]));  // (not sunk below the wait)
+      // the tile that used this buffer before
+      const int b = i - L::AS;
+      if (b >= 0 && !w4_wait_warp(done + 8 * (b % L::XS), (b / L::XS) & 1, budget, status, abort)) break;
+      tc_fence_after();
+      tmem_st_x16(col, v0);
+      tmem_st_x16(col + 16, v1);
+      values(2, v0);
+      tmem_st_x16(col + 32, v0);
+      values(3, v1);
+      tmem_st_x16(col + 48, v1);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(a_full + 8 * as);
       if ((rs += 2) >= L::RS) rs -= L::RS, rp ^= 1;
-      if ((as += 2) >= L::AS) as -= L::AS, ap ^= 1;
+      if ((as += 2) >= L::AS) as -= L::AS;
     }
   } else if (warp == L::MMA_WARP) {
     // ---- MMA issue (see mma_f16_ts: the whole warp, one lane elected)
@@ -289,13 +294,18 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     const uint64_t desc0 = sdesc_k_sw128(sbase + L::X);
     const bool short_tail = p.w.K - static_cast<int64_t>(kt0 + n - 1) * kW4K <= 64;  // one box in the last tile
     uint32_t xs = 0, as = 0, xp = 0, ap = 0;
+    bool ready = false;  // the tile's operands were seen to be there while the tile before was being issued
     for (int i = 0; i < n; ++i) {
-      if (!w4_wait_warp(a_full + 8 * as, ap, budget, status, abort)) break;
-      if (!w4_wait_warp(x_full + 8 * xs, xp, budget, status, abort)) break;
+      if (!ready) {
+        if (!w4_wait_warp(a_full + 8 * as, ap, budget, status, abort)) break;
+        if (!w4_wait_warp(x_full + 8 * xs, xp, budget, status, abort)) break;
+      }
       tc_fence_after();
       if (p.offsets) fence_proxy_async_smem();  // cp.async rows, visible to this thread, to the MMA's reads
       const uint64_t b0 = desc0 + xs * (L::XSTAGE >> 4);
-      const uint32_t a0 = tmem + L::A0 + as * (RT * kACols);
+      const uint32_t a0 = tmem + L::A0 + as * (RT * kACols), mine = done + 8 * xs;
+      if (++xs == L::XS) xs = 0, xp ^= 1;
+      if (++as == L::AS) as = 0, ap ^= 1;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j == 4 && short_tail && i == n - 1) break;  // (the A columns past K are zero, the B rows were not copied)
@@ -303,13 +313,10 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
 #pragma unroll
         for (int t = 0; t < RT; ++t)
           mma_f16_ts(tmem + t * BT, a0 + t * kACols + 8 * j, b, idesc, i > 0 || j > 0, leader);
+        if (j == 6)
+          ready = __all_sync(0xffffffffu, i + 1 < n && mbar_try_wait(a_full + 8 * as, ap) && mbar_try_wait(x_full + 8 * xs, xp));
       }
-      if (leader) {
-        mma_commit(a_empty + 8 * as);
-        mma_commit(x_empty + 8 * xs);
-      }
-      if (++xs == L::XS) xs = 0, xp ^= 1;
-      if (++as == L::AS) as = 0, ap ^= 1;
+      if (leader) mma_commit(mine);
     }
     if (leader) mma_commit(d_full);  // also after a wait that ran out: nothing in flight is left behind
   } else if (warp == L::REC_WARP) {
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       int issued = 0;
       uint32_t xs = 0, xp = 1;
       for (int i = 0; i < n; ++i) {
-        if (!w4_wait(x_empty + 8 * xs, xp, budget, status, abort)) break;
+        if (!w4_wait(done + 8 * xs, xp, budget, status, abort)) break;
         const uint32_t stage = sbase + L::X + xs * L::XSTAGE, bar = x_full + 8 * xs;
         const int32_t k = (kt0 + i) * kW4K;
         // the second box of a short last tile may lie past K altogether: it is
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     int64_t left = p.w.K - static_cast<int64_t>(kt0) * kW4K - 8 * c;
     uint32_t xs = 0, xp = 1;
     for (int i = 0; i < n; ++i) {
-      if (!w4_wait_warp(x_empty + 8 * xs, xp, budget, status, abort)) break;
+      if (!w4_wait_warp(done + 8 * xs, xp, budget, status, abort)) break;
       const uint32_t dst = sbase + L::X + xs * L::XSTAGE + at;
       const uint32_t mask = left > 0 ? live : 0;  // past K: zeros, and no address is read
 #pragma unroll
