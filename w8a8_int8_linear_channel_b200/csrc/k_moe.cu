@@ -27,16 +27,10 @@ __device__ __forceinline__ void warp_argmax(double& v, int& i) {
   }
 }
 
-// One warp per token; lane l holds experts 32 v + l.  Scores are formed in
-// 64 bits: which experts a token goes to must not hang on the last bits of a
-// 32-bit exponential, and two choices may lie arbitrarily close.
+// The whole definition in 64 bits, for any token; lane l holds experts 32 v + l.
+// c: room for E choices, used for group scores.
 template <int V>
-__global__ void __launch_bounds__(kRouteWarps * 32) k_moe_route(const RouteArgs a) {
-  extern __shared__ double sh[];  // [warps][E] choices, used for group scores
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  griddep_wait();
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
-  if (t >= a.T) return;
+__device__ __noinline__ void route_exactly(const RouteArgs& a, int64_t t, int lane, double* c) {
   const int E = a.E;
 
   double p[V], choice[V];
@@ -84,7 +78,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_moe_route(const RouteArgs 
   }
 
   if (a.topk_group < a.n_group) {
-    double* c = sh + warp * E;
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (32 * v + lane < E) c[32 * v + lane] = choice[v];
@@ -157,6 +150,231 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_moe_route(const RouteArgs 
   }
 }
 
+// Sortable bits of a float (no NaN).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t k) {
+  return __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xffffffffu));
+}
+constexpr uint32_t kNegInfKey = 0x007fffffu;  // order_key(-inf)
+
+// Lane l holds experts V l .. V l + V - 1; logits masked as in route_exactly.
+template <int V>
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, int lane, float (&l)[V]) {
+  const int e0 = lane * V;
+  const int bytes = a.half ? 2 : 4;
+  const char* row = static_cast<const char*>(a.logits) + t * a.ld * bytes;
+  if (V * bytes % 16 == 0 && (a.ld * bytes) % 16 == 0 && a.E % V == 0) {
+    // 16 bytes at a time: 8 (4) experts, all of them below E or none
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+      if (e0 + v < a.E) {
+        if (!a.half) {
+          const float4 f = *reinterpret_cast<const float4*>(row + (e0 + v) * 4);
+          l[v] = f.x, l[(v + 1) % V] = f.y, l[(v + 2) % V] = f.z, l[(v + 3) % V] = f.w;
+        } else {
+          const uint2 f = *reinterpret_cast<const uint2*>(row + (e0 + v) * 2);
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&f.x));
+          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f.y));
+          l[v] = x.x, l[(v + 1) % V] = x.y, l[(v + 2) % V] = y.x, l[(v + 3) % V] = y.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[(v + i) % V] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      l[v] = -INFINITY;
+      if (e0 + v < a.E)
+        l[v] = a.half ? __half2float(reinterpret_cast<const __half*>(row)[e0 + v])
+                      : reinterpret_cast<const float*>(row)[e0 + v];
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (isnan(l[v])) l[v] = -INFINITY;
+}
+
+// The same choice from 32-bit scores, whenever they are far enough apart to be
+// sure of it; false otherwise, and nothing is written.
+//
+// Without a bias and groups the choices are in the order of the logits, which
+// needs no score at all (as long as 64-bit scores of different logits differ:
+// sigmoids of logits up to 30, exponentials down to exp(-600)).  With them, a 32-bit choice is within
+// 2^-18 + 2^-19 |c| of the exact one: the exponential is off by 2^-20 relatively
+// (its argument up to 2^-19 where the score is then next to 0 or 1), a sum of up to 512 exponentials by
+// 2^-19, and score and choice are rounded.  Two choices (a group's score is one or two of them)
+// whose 32-bit values differ by more than four times that are in their exact order.  With
+// 256 experts under a bias about one token in fifty is not sure.
+template <int V>
+__device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, int lane) {
+  const int E = a.E;
+  const bool groups = a.topk_group < a.n_group;
+  const int per = E / a.n_group, lanes = per / V;  // lanes per group
+  if (groups && (lanes * V != per || (lanes & (lanes - 1)))) return false;
+  float l[V], c[V];
+  load_logits<V>(a, t, lane, l);
+  float top = -INFINITY;
+#pragma unroll
+  for (int v = 0; v < V; ++v) top = fmaxf(top, l[v]);
+  top = order_value(__reduce_max_sync(kAll, order_key(top)));
+  if (a.sigmoid ? !(top <= 30.0f) : !(top < INFINITY)) return false;  // (all masked: -inf passes)
+  const bool scores = groups || a.bias;
+  if (scores) {
+    if (top == -INFINITY) return false;
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      c[v] = a.sigmoid ? __fdividef(1.0f, __fadd_rn(1.0f, __expf(-l[v]))) : __expf(__fadd_rn(l[v], -top));
+      sum = __fadd_rn(sum, c[v]);
+    }
+    float scale = 1.0f;
+    if (!a.sigmoid) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(kAll, sum, o));
+      scale = __fdividef(1.0f, sum);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = lane * V + v;
+      c[v] = __fmul_rn(c[v], scale);
+      if (a.bias && e < E) c[v] = __fadd_rn(c[v], a.bias[e]);
+      if (l[v] == -INFINITY || isnan(c[v])) c[v] = -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = l[v];
+  }
+  auto apart = [](float larger, float smaller) {
+    return __fadd_rn(larger, -smaller) > 0x1p-16f + 0x1p-17f * fmaxf(fabsf(larger), fabsf(smaller));
+  };
+
+  if (groups) {
+    float first = -INFINITY, second = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      second = fmaxf(second, fminf(first, c[v]));
+      first = fmaxf(first, c[v]);
+    }
+    for (int o = 1; o < lanes; o <<= 1) {
+      const float f = __shfl_xor_sync(kAll, first, o), s2 = __shfl_xor_sync(kAll, second, o);
+      second = fmaxf(fmaxf(second, s2), fminf(first, f));
+      first = fmaxf(first, f);
+    }
+    float score = a.group_top == 2 && second > -INFINITY ? __fadd_rn(first, second) : first;
+    if (lane * V >= E) score = -INFINITY;
+    bool keep = false;
+    float before = INFINITY;
+    for (int j = 0; j <= a.topk_group; ++j) {
+      const uint32_t key = order_key(score), best = __reduce_max_sync(kAll, key);
+      const float value = order_value(best);
+      if (best == kNegInfKey) break;
+      if (j == a.topk_group) {
+        if (!apart(before, value)) return false;  // the last group kept and the first one left out
+        break;
+      }
+      before = value;
+      const int src = __ffs(__ballot_sync(kAll, key == best)) - 1;
+      if ((lane & ~(lanes - 1)) == (src & ~(lanes - 1))) {
+        keep = true;
+        score = -INFINITY;
+      }
+    }
+    if (!keep) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = -INFINITY;
+    }
+  }
+
+  // topk rounds of the warp's largest choice (ties to the lowest lane and, in
+  // it, the lowest expert); lane j keeps the j-th expert
+  // (32-bit scores give up the bits of their keys that then say which of the
+  // lane's experts it is; 2^-19 |c| at most, which `apart` allows for)
+  uint32_t key[V], mine = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    key[v] = order_key(c[v]);
+    if (scores && key[v] != kNegInfKey) key[v] = (key[v] & ~static_cast<uint32_t>(V - 1)) | (V - 1 - v);
+    mine = max(mine, key[v]);
+  }
+  int my_id = -1;
+  float before = INFINITY;
+  for (int j = 0; j < a.topk + (scores ? 1 : 0); ++j) {
+    const uint32_t best = __reduce_max_sync(kAll, mine);
+    if (best == kNegInfKey) break;
+    if (scores) {
+      const float value = order_value(best);
+      if (j > 0 && !apart(before, value)) return false;
+      before = value;
+      if (j == a.topk) break;
+    }
+    const int src = __ffs(__ballot_sync(kAll, mine == best)) - 1;
+    int at = V - 1 - static_cast<int>(best & (V - 1)), id = src * V + at;
+    if (!scores) {
+#pragma unroll
+      for (int v = V - 1; v >= 0; --v)
+        if (key[v] == best) at = v;
+      id = __shfl_sync(kAll, lane * V + at, src);
+    }
+    if (lane == j) my_id = id;
+    if (lane == src) {
+      mine = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (v == at) key[v] = 0;
+        mine = max(mine, key[v]);
+      }
+      mine = max(mine, kNegInfKey);
+    }
+  }
+  float my_logit = 0.0f;
+  if (my_id >= 0)
+    my_logit = a.half ? __half2float(static_cast<const __half*>(a.logits)[t * a.ld + my_id])
+                      : static_cast<const float*>(a.logits)[t * a.ld + my_id];
+  if (!scores && !a.sigmoid && __any_sync(kAll, my_id >= 0 && my_logit < top - 600.0f)) return false;
+
+  // the chosen experts' weights, in 64 bits
+  double p = 0.0;
+  if (my_id >= 0)
+    p = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(my_logit)))
+                  : exp(static_cast<double>(my_logit) - static_cast<double>(top));
+  double sum = 1.0;
+  if (a.renormalize || !a.sigmoid) {
+    sum = p;
+    if (!a.renormalize) {
+      sum = 0.0;  // the softmax's own sum
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (l[v] != -INFINITY) sum += exp(static_cast<double>(l[v]) - static_cast<double>(top));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  }
+  if (lane < a.topk) {
+    a.ids[t * a.topk + lane] = my_id;
+    a.weights[t * a.topk + lane] = static_cast<float>((sum > 0.0 ? p / sum : 0.0) * a.scale);
+  }
+  return true;
+}
+
+// One warp per token.  Scores count in 64 bits: which experts a token goes to
+// must not hang on the last bits of a 32-bit exponential, and two choices may
+// lie arbitrarily close.  Most tokens can be decided without forming them.
+// 8192 tokens, 256 experts in 8 groups, under a bias: 28.9 us all in 64 bits.
+template <int V>
+__global__ void __launch_bounds__(kRouteWarps * 32) k_moe_route(const RouteArgs a) {
+  extern __shared__ double sh[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_wait();
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp;
+  if (t >= a.T) return;
+  if (!route_fast<V>(a, t, lane)) route_exactly<V>(a, t, lane, sh + warp * a.E);
+}
+
 // ------------------------------------------------------------------ plan ----
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
@@ -213,6 +431,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     int32_t before = 0, all = here;
     if (chunks > 1) {
       all = 0;
+#pragma unroll 8
       for (int c = 0; c < chunks; ++c) {
         const int32_t n = counts[static_cast<int64_t>(c) * E + e];
         if (c < static_cast<int>(blockIdx.x)) before += n;

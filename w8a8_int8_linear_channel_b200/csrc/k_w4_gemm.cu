@@ -289,7 +289,9 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     }
   } else if (warp == L::MMA_WARP) {
     // ---- MMA issue (see mma_f16_ts: the whole warp, one lane elected)
-    constexpr uint32_t idesc = idesc_f16(kW4Rows, BT);
+    // (a block that is not full, the last one of an expert or of all tokens, takes
+    // as many columns as it has tokens, in sixteens)
+    const uint32_t idesc = idesc_f16(kW4Rows, (count + 15) & ~15);
     const uint32_t leader = elect_one();
     const uint64_t desc0 = sdesc_k_sw128(sbase + L::X);
     const bool short_tail = p.w.K - static_cast<int64_t>(kt0 + n - 1) * kW4K <= 64;  // one box in the last tile
@@ -383,6 +385,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       const uint32_t mask = left > 0 ? live : 0;  // past K: zeros, and no address is read
 #pragma unroll
       for (int j = 0; j < BT / 8; ++j) {
+        if (8 * j >= count) break;  // rows that no MMA reads but the last sixteen's rest, whose columns go nowhere
         const bool on = mask >> j & 1;
         cp_async16(dst + j * 1024, on ? src[j] : p.x, on ? 16 : 0);
         src[j] += kW4K;

@@ -23,20 +23,29 @@ GROUPS = (32, 64, 128)
 # look at the current device per call, plain integers as pointers, and the
 # current stream's handle without a Stream object where torch offers it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
 
 
 def _ptrs(*tensors):
     """Device addresses (None stays None); a host tensor or one on another GPU is refused as by _p."""
-    first = next(t for t in tensors if t is not None)
-    dev = torch.cuda.current_device() if first.is_cuda else -2
-    return [None if t is None else (t.data_ptr() if t.get_device() == dev else _p(t)) for t in tensors]
+    dev = -2
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if dev == -2 and t.is_cuda:
+            dev = _current_device()
+        out.append(t.data_ptr() if t.get_device() == dev else _p(t))
+    return out
 
 
 def _stream(stream) -> int:
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -81,7 +90,7 @@ def _dense(w4: W4Weight, what: str) -> None:
 
 def _tensor(t: torch.Tensor, dtype, shape: tuple, name: str) -> None:
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: need a contiguous {dtype} {shape} tensor")
+        raise ValueError(f"{name}: need a contiguous {dtype} {tuple(shape)} tensor")
 
 
 def sq_quantize_weight_w4(w: torch.Tensor, w4: W4Weight, s=None, stream=None) -> W4Weight:
@@ -131,17 +140,26 @@ def sq_w4_dequantize(w4: W4Weight, out: torch.Tensor, stream=None) -> torch.Tens
 def sq_w4a16_linear(x: torch.Tensor, w4: W4Weight, y: torch.Tensor, bias=None, relu: bool = False,
                     stream=None) -> torch.Tensor:
     """y fp16 [M, N] = fp16(x @ W^T + bias) with a packed 4-bit W; ReLU optional."""
-    _dense(w4, "sq_w4a16_linear")
-    M, K, ld = _rows(x, torch.float16, "x")
-    if K != w4.K:
-        raise ValueError(f"x: need [M, {w4.K}], got {tuple(x.shape)}")
-    if M == 1:
-        ld = max(ld, K)  # the stride of a single row means nothing
-    _vec(bias, w4.N, torch.float16, "bias")
-    _tensor(y, torch.float16, (M, w4.N), "y")
-    px, pw, pb, py = _ptrs(x, w4.packed, bias, y)
-    _check(_L.sq_w4a16_linear(px, M, ld, pw, w4.N, K, w4.group, w4.zero_point, pb, bool(relu), py, _stream(stream)),
-           "sq_w4a16_linear")
+    if w4.experts is not None:
+        _dense(w4, "sq_w4a16_linear")
+    shape = x.shape
+    if x.dtype != _F16 or len(shape) != 2:
+        _rows(x, _F16, "x")
+    M, K = shape
+    ld, inner = x.stride()
+    N = w4.N
+    if K != w4.K or inner != 1:
+        raise ValueError(f"x: need [M, {w4.K}] with a unit inner stride, got {tuple(shape)}")
+    if M == 1 and ld < K:
+        ld = K  # the stride of a single row means nothing
+    if y.dtype != _F16 or y.shape != (M, N) or not y.is_contiguous():
+        _tensor(y, _F16, (M, N), "y")
+    if bias is not None:
+        _vec(bias, N, _F16, "bias")
+    px, pw, py, pb = _ptrs(x, w4.packed, y, bias)
+    status = _L.sq_w4a16_linear(px, M, ld, pw, N, K, w4.group, w4.zero_point, pb, bool(relu), py, _stream(stream))
+    if status:
+        _check(status, "sq_w4a16_linear")
     return y
 
 
@@ -153,21 +171,25 @@ def sq_moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
                  scale: float = 1.0, stream=None):
     """The topk experts of every token (ids int32 [T, topk], largest choice first) and their weights
     (fp32 [T, topk]) from router logits, fp32 or fp16 [T, E]."""
-    if logits.dtype not in (torch.float32, torch.float16):
+    half = logits.dtype == _F16
+    if not half and logits.dtype != _F32:
         raise ValueError("logits: fp32 or fp16")
     if score not in _SCORES:
         raise ValueError(f"score: one of {sorted(_SCORES)}")
     T, E, ld = _rows(logits, logits.dtype, "logits")
-    if ids.dim() != 2 or ids.shape[0] != T:
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != T:
         raise ValueError(f"ids: need [{T}, topk]")
-    topk = ids.shape[1]
-    _tensor(ids, torch.int32, (T, topk), "ids")
-    _tensor(weights, torch.float32, (T, topk), "weights")
-    _vec(bias, E, torch.float32, "bias")
-    pl, pb, pi, pw = _ptrs(logits, bias, ids, weights)
-    _check(_L.sq_moe_route(pl, logits.dtype == torch.float16, T, E, max(ld, E) if T == 1 else ld, pb, _SCORES[score],
-                           n_group, topk_group, group_top, topk, bool(renormalize), scale, pi, pw, _stream(stream)),
-           "sq_moe_route")
+    topk = shape[1]
+    _tensor(ids, _I32, shape, "ids")
+    _tensor(weights, _F32, shape, "weights")
+    if bias is not None:
+        _vec(bias, E, _F32, "bias")
+    pl, pi, pw, pb = _ptrs(logits, ids, weights, bias)
+    status = _L.sq_moe_route(pl, half, T, E, max(ld, E) if T == 1 else ld, pb, _SCORES[score], n_group, topk_group,
+                             group_top, topk, bool(renormalize), scale, pi, pw, _stream(stream))
+    if status:
+        _check(status, "sq_moe_route")
     return ids, weights
 
 
