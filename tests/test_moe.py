@@ -245,7 +245,8 @@ def _experts(x, w, group, ids, E, div, bias=None, relu=False, f32=False):
                                                      (7, 3, 5, 128, 512, 128, False), (40, 4, 6, 200, 144, 32, True),
                                                      (64, 2, 3, 260, 256, 128, True), (300, 4, 8, 96, 528, 64, False),
                                                      (700, 2, 2, 136, 128, 128, False), (20, 2, 2, 130, 4112, 32, True),
-                                                     (512, 2, 4, 3400, 1040, 64, True)])
+                                                     (512, 2, 4, 3400, 1040, 64, True),
+                                                     (48, 2, 8, 300, 528, 32, True), (400, 8, 150, 140, 144, 64, False)])
 def test_experts(cuda_device, T, topk, E, N, K, group, zero):
     rng = np.random.default_rng(T + N)
     w = ref.random_weight(rng, N, K, group, zero, lead=(E,))

@@ -219,6 +219,19 @@ def test_linear(cuda_device, M, N, K, group, zero):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("M,N,K", [(10, 5000, 2064), (33, 2100, 2320), (64, 1000, 5008), (65, 1100, 2192),
+                                   (130, 777, 2320), (500, 900, 592), (1000, 3000, 272)])
+def test_linear_many_tokens(cuda_device, M, N, K, group, zero):
+    # enough work for the kernel of many tokens whatever their number: odd sizes, one and two weight tiles
+    rng = np.random.default_rng(M * 1000 + N + K)
+    w = ref.random_weight(rng, N, K, group, zero)
+    bias = rng.standard_normal(N).astype(np.float16) if M % 2 else None
+    _check_linear(_tokens(rng, M, K), w, group, bias, relu=M % 3 == 0, ldx=K + 24 if M % 4 else None)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (4, 64, 49152), (16, 1000, 12288), (32, 49152, 256),
                                    (128, 512, 4096), (1000, 777, 4112), (2048, 256, 512), (640, 7700, 144),
                                    (1280, 4000, 1040), (40, 130, 8208)])
@@ -228,15 +241,16 @@ def test_linear_larger(cuda_device, M, N, K):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [3, 16, 40, 200])
-def test_linear_nonfinite_tokens_stay_in_their_row(cuda_device, M):
+@pytest.mark.parametrize("M,N,K", [(3, 140, 272), (16, 140, 272), (40, 140, 272), (200, 140, 272),
+                                   (40, 2100, 2320), (200, 2100, 528), (1500, 2100, 272)])
+def test_linear_nonfinite_tokens_stay_in_their_row(cuda_device, M, N, K):
     import w8a8_int8_linear_channel_b200 as sq
     rng = np.random.default_rng(M)
-    N, K, group = 140, 272, 64
+    group = 64
     w = ref.random_weight(rng, N, K, group, True)
     x = _tokens(rng, M, K)
     y0 = host(_check_linear(x, w, group))
-    x[1, 270], x[2, 0] = np.nan, np.inf
+    x[1, K - 2], x[2, 0] = np.nan, np.inf
     y = torch.empty((M, N), dtype=torch.float16, device="cuda")
     sq.sq_w4a16_linear(dev(x), _pack(w, group), y)
     got = host(y)
@@ -248,11 +262,11 @@ def test_linear_nonfinite_tokens_stay_in_their_row(cuda_device, M):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [1, 24, 150])
-def test_linear_overflow_and_zero_scales(cuda_device, M):
+@pytest.mark.parametrize("M,N", [(1, 130), (24, 130), (150, 130), (24, 25000), (150, 8000), (500, 8000)])
+def test_linear_overflow_and_zero_scales(cuda_device, M, N):
     # sums past 65504 become Inf; groups of scale 0 contribute nothing
     import w8a8_int8_linear_channel_b200 as sq
-    N, K, group = 130, 160, 32
+    K, group = 160, 32
     codes = np.full((N, K), 15, np.uint8)
     scales = np.full((N, 5), 64.0, np.float16)
     scales[1] = 0
@@ -265,13 +279,13 @@ def test_linear_overflow_and_zero_scales(cuda_device, M):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M", [1, 13, 30, 90, 300])
-def test_linear_streams_graphs_and_repeats(cuda_device, M):
+@pytest.mark.parametrize("M,N", [(1, 520), (13, 520), (30, 520), (90, 520), (300, 520), (20, 8001), (128, 8008)])
+def test_linear_streams_graphs_and_repeats(cuda_device, M, N):
     """The same bits from: a repeated call, another stream, two streams at once, a captured and
     replayed call whose input changed, and an output inside guard bands."""
     import w8a8_int8_linear_channel_b200 as sq
     rng = np.random.default_rng(M)
-    N, K, group = 520, 2064, 128
+    K, group = 2064, 128
     w4 = _pack(ref.random_weight(rng, N, K, group, True), group)
     xa, xb = dev(_tokens(rng, M, K)), dev(_tokens(rng, M, K))
     new = lambda: torch.full((M, N), float("nan"), dtype=torch.float16, device="cuda")
@@ -323,13 +337,14 @@ def test_w4_linear_layer(cuda_device):
 
 
 @pytest.mark.gpu
-def test_wait_that_runs_out_is_reported(cuda_device):
+@pytest.mark.parametrize("M", [4, 40, 300])
+def test_wait_that_runs_out_is_reported(cuda_device, M):
     """With the smallest wait budget a call may give up; it must say so or be right."""
     import w8a8_int8_linear_channel_b200 as sq
     rng = np.random.default_rng(8)
-    w = ref.random_weight(rng, 512, 4096, 128, False)
-    w4, x = _pack(w, 128), dev(_tokens(rng, 4, 4096))
-    good = sq.sq_w4a16_linear(x, w4, torch.empty((4, 512), dtype=torch.float16, device="cuda"))
+    w = ref.random_weight(rng, 2048, 4096, 128, False)
+    w4, x = _pack(w, 128), dev(_tokens(rng, M, 4096))
+    good = sq.sq_w4a16_linear(x, w4, torch.empty((M, 2048), dtype=torch.float16, device="cuda"))
     torch.cuda.synchronize()
     try:
         sq.sq_set_wait_budget_ns(1000)

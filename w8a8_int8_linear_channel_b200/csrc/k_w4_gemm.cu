@@ -70,17 +70,7 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Columns [col, col + 8 or 16) of the warp's lanes, complete on return.
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
-               :
-               : "memory");
-}
+// Columns [col, col + 16) of the warp's lanes, complete on return.
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
   tmem_ld_32x32b_x16(taddr, r);
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -120,8 +110,8 @@ struct Layout {
   static constexpr int THREADS = X_WARP * 32 + X_THREADS;
   static constexpr int REC = w4_record_bytes(G, ZERO);
   static constexpr int XSTAGE = BT * kW4K * 2;             // two boxes of [BT][64 k], 128-byte swizzle
-  static constexpr int XS = BT <= 64 ? 4 : RT == 2 ? 4 : 2;  // token stages
-  static constexpr int RS = BT <= 32 ? 7 : 4;               // record stages, RT records each
+  static constexpr int XS = BT == 64 || RT == 2 ? 4 : 2;  // token stages
+  static constexpr int RS = 4;                            // record stages, RT records each
   static constexpr int AS = RT == 2 || BT == 128 ? 2 : 3;  // operand buffers in tensor memory
   static constexpr int D_COLS = RT * BT;
   static constexpr int A0 = D_COLS;
@@ -420,7 +410,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     float bias = 0.0f;
     if (p.bias && ch < p.w.N) bias = __half2float(p.bias[static_cast<int64_t>(expert) * p.w.N + ch]);
     const int share = (kW4Rows + slices - 1) / slices;
-    constexpr int STEP = BT == 16 ? 8 : 16;
+    constexpr int STEP = 16;
     for (int col = c0; col < c1; col += STEP) {
       if (col >= count) break;  // no token of this block lies there
       __syncwarp();
@@ -504,6 +494,25 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   if (warp == L::MMA_WARP) tmem_dealloc(tmem, L::TMEM_COLS);
 }
 
+// Slices of K per weight tile (the cluster size).  A CTA's time is taken as 0.39 us per K tile and 64
+// tokens, 4.5 for start and finish and 4 more for the cluster's sum (4096 x
+// 4096 at 64 tokens: 17.0 us with one slice, 11.5 with four).  Two CTAs on an
+// SM overlap their tiles, hardly the rest: with clusters until every SM has
+// two, 4096 x 4096 at 384 tokens took 41.1 us, with one slice 26.4.  Clusters
+// of more than two do not pack every SM of a GPC; an eighth is taken off
+// (4096 x 16384 at 384 tokens: 288 CTAs in threes 86.7 us, in twos 70.3).
+int pick_slices(int64_t units, int64_t kt, int bt, int num_sms) {
+  int slices = 1;
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= kMaxSlices && (s == 1 || kt / s >= 4); ++s) {
+    const int64_t sms = s <= 2 ? num_sms : num_sms - num_sms / 8;
+    const int64_t per_sm = (units * s + sms - 1) / sms;
+    const int64_t cost = (per_sm + 1) / 2 * ((kt + s - 1) / s) * (bt / 64) * 39 + per_sm * (s == 1 ? 450 : 850);
+    if (cost < best) best = cost, slices = s;
+  }
+  return slices;
+}
+
 template <int BT, int RT, int G, bool ZERO>
 cudaError_t launch(const W4Product& p, const Ctx& c) {
   using L = Layout<BT, RT, G, ZERO>;
@@ -517,7 +526,7 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   if (!p.offsets && !make_tmap_f16_rows(&tm, p.x, p.M, p.w.K, p.ldx, BT)) return cudaErrorUnknown;
   const int64_t tiles = (p.w.nt() + RT - 1) / RT, kt = p.w.kt();
   const int64_t blocks = w4_blocks(p, BT);
-  const int slices = RT == 2 ? 1 : w4_slices(tiles * blocks, kt, static_cast<int64_t>(c.num_sms) * per_sm, 6);
+  const int slices = RT == 1 ? pick_slices(tiles * blocks, kt, BT, c.num_sms) : 1;
   if (tiles * blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * blocks * slices));
@@ -552,9 +561,13 @@ cudaError_t launch_g(const W4Product& p, const Ctx& c) {
 }  // namespace
 
 cudaError_t launch_w4_gemm(const W4Product& p, const Ctx& c, int64_t tokens) {
-  if (tokens <= 16) return launch_g<16, 1>(p, c);
-  if (tokens <= 32) return launch_g<32, 1>(p, c);
-  if (tokens <= 64) return launch_g<64, 1>(p, c);
+  // Blocks of 64 tokens or 128.  A block's MMAs are only as wide as it has
+  // tokens, so narrower blocks would save nothing (16384 x 4096 at 16 tokens
+  // takes 17.2 us with blocks of 16, 32 or 64).  An expert's tokens scatter around the average, and a
+  // second block makes its weight's operand once more: 64 experts with 12
+  // tokens each, blocks of 16 / 32 / 64 / 128: 273 / 239 / 225 / 231 us a layer, with 20:
+  // 376 / 262 / 243 / 239, with 32: 500 / 329 / 270 / 252.
+  if (tokens <= (p.offsets ? 16 : 64)) return launch_g<64, 1>(p, c);
   // two weight tiles per CTA halve the token traffic, if enough CTAs are left
   if (w4_blocks(p, 128) * ((p.w.nt() + 1) / 2) >= c.num_sms) return launch_g<128, 2>(p, c);
   return launch_g<128, 1>(p, c);

@@ -366,23 +366,24 @@ int64_t w4_blocks(const W4Product& p, int bt) {
   return p.M < blocks + p.E ? p.M : blocks + p.E;
 }
 
-int w4_slices(int64_t units, int64_t kt, int64_t slots, int start_tiles) {
-  int slices = 1;
-  int64_t best = INT64_MAX;
-  for (int s = 1; s <= kMaxSlices && (s == 1 || kt / s >= 4); ++s) {
-    const int64_t cost = ((units * s + slots - 1) / slots) * ((kt + s - 1) / s + start_tiles);
-    if (cost < best) {
-      best = cost;
-      slices = s;
-    }
-  }
-  return slices;
-}
+// Which kernel.  Up to eight tokens per weight tile always this one.  With
+// more it reads the weight once per eight tokens, which still pays where an SM
+// has little to do altogether (starting the tensor cores' pipeline takes 3 us
+// longer): 1024 x 1024 at 64 tokens 3.4 us here, 9.9 there; 4096 x 4096 at 16
+// tokens 7.1 and 9.1, at 24 10.2 and 9.5; 4096 x 16384 at 16 29.4 and 19.8.
+// Experts' tokens scatter around the average (most of them still need one
+// block of eight): 64 experts with 10 tokens each 210 us a layer here and 222
+// there, with 12 242 and 225; 256 small experts with 10 122 and 129, with 16
+// 162 and 136.
+constexpr int kTilesPerSm = 32;    // 64 channels x 128 k x eight tokens
+constexpr int kTokensExperts = 10;
 
 cudaError_t launch_w4_product(const W4Product& p, const Ctx& c) {
   // the tokens that share a weight tile: for experts the average
   const int64_t tokens = p.offsets ? (p.M + p.E - 1) / p.E : p.M;
-  return tokens <= kTokens ? launch_w4_stream(p, c) : launch_w4_gemm(p, c, tokens);
+  const int64_t work = w4_blocks(p, kTokens) * 2 * p.w.nt() * p.w.kt();  // 64-channel K tiles
+  const bool stream = tokens <= kTokens || (p.offsets ? tokens <= kTokensExperts : work <= kTilesPerSm * c.num_sms);
+  return stream ? launch_w4_stream(p, c) : launch_w4_gemm(p, c, tokens);
 }
 
 }  // namespace sq

@@ -83,16 +83,11 @@ struct W4Product {
   int div;
 };
 cudaError_t launch_w4_product(const W4Product& p, const Ctx& c);
-cudaError_t launch_w4_stream(const W4Product& p, const Ctx& c);                  // up to eight tokens per weight tile
-cudaError_t launch_w4_gemm(const W4Product& p, const Ctx& c, int64_t tokens);    // more
+cudaError_t launch_w4_stream(const W4Product& p, const Ctx& c);                // few tokens per weight tile
+cudaError_t launch_w4_gemm(const W4Product& p, const Ctx& c, int64_t tokens);  // more; tokens per tile on average
 // Blocks of bt tokens: exactly, or for experts the most that any routing of
 // the pairs can need (CTAs of blocks that do not exist leave at once).
 int64_t w4_blocks(const W4Product& p, int bt);
-// Slices of K per weight tile (the cluster size, at most 8) that give the
-// shortest busiest slot: waves of CTAs times the tiles of one, plus
-// start_tiles tiles' worth of start and finish per CTA; at least four tiles
-// per slice, ties to fewer slices.
-int w4_slices(int64_t units, int64_t kt, int64_t slots, int start_tiles);
 
 // Expert routing (k_moe.cu).
 struct RouteArgs {
