@@ -156,6 +156,23 @@ def test_route_ties_take_the_lowest_index(cuda_device):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_different_logits_whose_64_bit_scores_tie(cuda_device, score):
+    rng = np.random.default_rng(23)
+    E, topk = 64, 6
+    step = np.stack([rng.permutation(E) for _ in range(7)]).astype(np.float32)
+    l = np.stack([step[0] * np.float32(1e-20),                  # next to 0: exp(l) == 1
+                  -800 - step[1],                               # sigmoids and exponentials that are 0 ...
+                  np.where(step[2] < 3, step[2], -800 - step[2]),  # ... for some of the chosen
+                  50 + step[3],                                 # sigmoids that are 1
+                  25 + step[4] * np.float32(2.0**-19),          # and some that 64 bits can hardly tell apart
+                  np.where(step[5] < 60, -5 - step[5], step[5] * np.float32(1e-21)),
+                  np.where(step[6] % 2 == 0, np.float32(0.0), np.float32(-0.0))]).astype(np.float32)
+    _check_route(l, topk, score=score)
+    _check_route(l, topk, score=score, renormalize=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_masked_and_nonfinite(cuda_device, score):
     rng = np.random.default_rng(11)
     E, topk = 40, 4
