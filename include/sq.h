@@ -423,8 +423,9 @@ sq_status sq_w8a8_linear_noalloc(const int8_t* xq, const float* x_scale, const i
  * be short.  Codes, scales and zero points live together in one packed buffer
  * of sq_w4_packed_bytes bytes, laid out once for the kernels (read it back
  * with sq_w4_dequantize); several experts' weights of one shape follow each
- * other in one buffer.
+ * other in one buffer.  K is a multiple of 16, N at most SQ_W4_MAX_N.
  */
+#define SQ_W4_MAX_N 8388480
 
 /* Bytes of one packed weight (0 for a shape no entry point takes). */
 size_t sq_w4_packed_bytes(int64_t N, int64_t K, int group, int has_zero);
@@ -437,7 +438,8 @@ size_t sq_w4_packed_bytes(int64_t N, int64_t K, int group, int has_zero);
  *   s = fp16( r7( (hi - lo) / 15 ) ),  z = min(rint(-lo / s), 15),
  *   q = clamp(rint(w' / s) + z, 0, 15)
  * where r8 / r7 round to 8 / 7 significant bits, so that every (q - z) * s is
- * exactly an fp16 number.  A group of zeros gets scale 0; a NaN never sets a
+ * exactly an fp16 number (unless it lies past fp16's range, which weights near
+ * the type's largest value can come to).  A group of zeros gets scale 0; a NaN never sets a
  * range and is coded as zero; an Inf gives scale Inf (its group's values are
  * then NaN).
  *   w fp16 [N, K]; s fp32 [K] or NULL; w4: the packed buffer
@@ -459,7 +461,11 @@ sq_status sq_w4_dequantize(const void* w4, int64_t N, int64_t K, int group, int 
  * The linear with a packed 4-bit weight, any number of tokens:
  *   y[m, n] = fp16( sum_k x[m, k] * W[n, k] + fp32(bias[n]) ),  max(., 0) before the
  * rounding when relu (a NaN becomes 0).  Sums are fp32.  Needs no workspace;
- * the same inputs give the same bits on every call.
+ * the same inputs give the same bits on every call (a row's bits may depend on
+ * the number of rows: few and many tokens take different kernels).  With many
+ * tokens W is rounded to fp16 once, as sq_w4_dequantize shows it, which changes
+ * nothing for weights from sq_quantize_weight_w4 or any scales of 7 significant
+ * bits.
  *   x fp16 [M, ldx], ldx >= K, ldx % 8 == 0; bias fp16 [N] or NULL; y fp16 [M, N]
  */
 sq_status sq_w4a16_linear(const void* x_f16, int64_t M, int64_t ldx, const void* w4, int64_t N, int64_t K, int group,
@@ -509,7 +515,8 @@ sq_status sq_moe_plan(const int32_t* ids, int64_t pairs, int64_t E, int32_t* off
  *   y[p, :] = x[p / pairs_per_row, :] W_e^T + bias[e, :]  (ReLU as in sq_w4a16_linear)
  * pairs_per_row is topk for the product on the tokens and 1 for one on an
  * earlier product's rows.  Rows of pairs that the plan leaves out are left as
- * they were.  Plan entries outside [0, pairs) are skipped.
+ * they were.  Plan entries outside [0, pairs) are skipped; of a pair that an
+ * order not from sq_moe_plan lists twice either result may stay.
  *   x fp16 [rows, ldx]; w4: E packed weights; bias fp16 [E, N] or NULL;
  *   y fp16 [pairs, N], or fp32 with y_f32 != 0
  */

@@ -22,7 +22,7 @@ def test_packed_bytes():
     f = _lib().sq_w4_packed_bytes
     assert f(128, 128, 128, 0) == 8192 + 256
     assert f(129, 144, 32, 1) == 4 * (8192 + 1024 + 512)
-    for bad in [(0, 128, 128, 0), (128, 120, 128, 0), (128, 0, 64, 0), (128, 128, 48, 0), (128, 133152, 32, 0)]:
+    for bad in [(0, 128, 128, 0), (128, 120, 128, 0), (128, 0, 64, 0), (128, 128, 48, 0), (128, 133152, 32, 0), (8388481, 16, 32, 0)]:
         assert f(*bad) == 0
 
 
@@ -61,7 +61,7 @@ def test_linear_refuses_on_the_host():
     assert with_(_0=None) == 1 and with_(_3=None) == 1 and with_(_10=None) == 1
     assert with_(_1=0) == 1 and with_(_4=0) == 1 and with_(_2=56) == 1     # M, N, ldx < K
     assert with_(_2=68) == 2 and with_(_0=FAKE_ODD) == 2 and with_(_8=FAKE_ODD) == 2 and with_(_10=FAKE_ODD) == 2
-    assert with_(_5=40) == 3 and with_(_6=100) == 3 and with_(_1=1 << 31) == 3
+    assert with_(_5=40) == 3 and with_(_6=100) == 3 and with_(_1=1 << 31) == 3 and with_(_4=8388481) == 3
     assert with_(_5=133152, _2=133152) == 4
 
 
@@ -136,6 +136,36 @@ def test_pack_and_dequantize(cuda_device, N, K, group, zero):
     out = torch.full((N, K), float("nan"), dtype=torch.float16, device="cuda")
     sq.sq_w4_dequantize(_pack(w, group), out)
     assert np.array_equal(host(out).astype(np.float64), ref.values(*w, group))
+
+
+@pytest.mark.gpu
+def test_pack_experts_on_another_stream(cuda_device):
+    # experts whose scales start off 16 bytes, filled in on the call's stream only after a while
+    import w8a8_int8_linear_channel_b200 as sq
+    rng = np.random.default_rng(3)
+    E, N, K, group = 3, 5, 48, 32
+    c, s, z = (dev(a) for a in ref.random_weight(rng, N, K, group, True, lead=(E,)))
+    want = sq.sq_w4_pack(c, s, sq.new_w4_weight(N, K, group, True, experts=E), z).packed
+    c2, s2, z2 = (torch.zeros_like(t) for t in (c, s, z))
+    w4 = sq.new_w4_weight(N, K, group, True, experts=E)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        c2.copy_(c), s2.copy_(s), z2.copy_(z)
+    sq.sq_w4_pack(c2, s2, w4, z2, stream=side)
+    side.synchronize()
+    assert torch.equal(w4.packed, want)
+
+
+@pytest.mark.gpu
+def test_more_blocks_than_a_grid_holds_is_refused(cuda_device):
+    # refused before any launch, and no error stays behind for the next call
+    x = torch.zeros((4, 64), dtype=torch.float16, device="cuda")
+    a = x.data_ptr()
+    assert _lib().sq_w4a16_linear(a, 0x7fffffff, 64, a, 8388480, 64, 32, 0, None, 0, a, None) == 3
+    torch.cuda.synchronize()
+    assert float(x.sum()) == 0.0
 
 
 @pytest.mark.gpu

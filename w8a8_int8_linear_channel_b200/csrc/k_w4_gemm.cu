@@ -518,9 +518,7 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   using L = Layout<BT, RT, G, ZERO>;
   auto kernel = k_w4_gemm<BT, RT, G, ZERO>;
   static KernelSetup setup;
-  int per_sm = 0;
-  const cudaError_t e =
-      kernel_setup(setup, reinterpret_cast<const void*>(kernel), L::THREADS, L::BYTES, c.device, &per_sm);
+  const cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(kernel), L::BYTES, c.device);
   if (e != cudaSuccess) return e;
   CUtensorMap tm = {};
   if (!p.offsets && !make_tmap_f16_rows(&tm, p.x, p.M, p.w.K, p.ldx, BT)) return cudaErrorUnknown;

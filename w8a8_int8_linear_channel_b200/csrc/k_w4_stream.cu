@@ -23,6 +23,7 @@
 // the cluster that finishes those channels (distributed shared memory), which
 // adds them in a fixed order: no atomics, no workspace, the same bits on every
 // run.
+#include "../../include/sq.h"
 #include "sq_w4.cuh"
 
 namespace sq {
@@ -310,8 +311,7 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   constexpr int kKGroups = kWarps / kRowGroups, kRows = kRowGroups * 32;
   constexpr size_t smem = kWarps * Ring<G, ZERO>::WARP;
   static KernelSetup setup;
-  int per_sm;
-  const cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(kernel), kThreads, smem, c.device, &per_sm);
+  const cudaError_t e = kernel_setup(setup, reinterpret_cast<const void*>(kernel), smem, c.device);
   if (e != cudaSuccess) return e;
   const int64_t nt = p.w.nt(), kt = p.w.kt();
   const int64_t blocks = w4_blocks(p, kTokens), units = (p.w.N + kRows - 1) / kRows;
@@ -320,6 +320,7 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   const int slices = pick_slices(units * likely, kt, kKGroups, c.num_sms);
   // ceil(2^16 / share): r * share_inv >> 16 is r / share for every channel r of the CTA
   const uint32_t share = (kRows + slices - 1) / slices, share_inv = (65536 + share - 1) / share;
+  static_assert(kRowGroups < 4 || SQ_W4_MAX_N <= 65535LL * kRows, "grid.y");
   if (units > 65535 || blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks * slices), static_cast<unsigned>(units));

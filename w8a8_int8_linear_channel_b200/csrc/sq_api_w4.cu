@@ -12,12 +12,10 @@ namespace {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }  // NULL is aligned
 
 sq_status launched(cudaError_t e) {
-  if (e == cudaErrorInvalidConfiguration) return SQ_ERR_UNSUPPORTED_SHAPE;  // more blocks than a grid holds
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return SQ_ERR_CUDA;
-  }
-  return SQ_OK;
+  if (e == cudaSuccess) return SQ_OK;
+  cudaGetLastError();
+  // more blocks than a grid holds
+  return e == cudaErrorInvalidConfiguration ? SQ_ERR_UNSUPPORTED_SHAPE : SQ_ERR_CUDA;
 }
 
 sq_status context(sq_stream_t stream, Ctx* c) { return static_cast<sq_status>(call_context(stream, c)); }
@@ -25,7 +23,7 @@ sq_status context(sq_stream_t stream, Ctx* c) { return static_cast<sq_status>(ca
 sq_status check_weight(const void* w4, int64_t N, int64_t K, int group, int has_zero, W4Weight* w) {
   if (!w4 || N <= 0 || K <= 0) return SQ_ERR_INVALID_ARG;
   if (K > SQ_MAX_K) return SQ_ERR_K_OVERFLOW;
-  if (K % 16 != 0 || N > 0x7fffffffLL) return SQ_ERR_UNSUPPORTED_SHAPE;
+  if (K % 16 != 0 || N > SQ_W4_MAX_N) return SQ_ERR_UNSUPPORTED_SHAPE;
   if (group != 32 && group != 64 && group != 128) return SQ_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(w4)) return SQ_ERR_MISALIGNED;
   w->data = static_cast<uint8_t*>(const_cast<void*>(w4));

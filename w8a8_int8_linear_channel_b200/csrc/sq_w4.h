@@ -42,23 +42,17 @@ struct W4Weight {
   int64_t bytes() const { return nt() * kt() * w4_record_bytes(group, zero); }
 };
 
-// Per kernel and device, once: allows `smem` bytes of dynamic shared memory and
-// counts the resident CTAs per SM.  A launch of a few microseconds should not
-// ask the runtime for either every time.
+// Per kernel and device, once: allows `smem` bytes of dynamic shared memory.  A
+// launch of a few microseconds should not ask the runtime for it every time.
 struct KernelSetup {
-  std::atomic<int> per_sm[64];  // 0: not asked yet
+  std::atomic<bool> done[64];
 };
-inline cudaError_t kernel_setup(KernelSetup& k, const void* kernel, int threads, size_t smem, int device, int* per_sm) {
-  int n = k.per_sm[device].load(std::memory_order_acquire);
-  if (n == 0) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
-    if (e != cudaSuccess) return e;
-    if (n < 1) return cudaErrorLaunchOutOfResources;
-    k.per_sm[device].store(n, std::memory_order_release);
-  }
-  *per_sm = n;
-  return cudaSuccess;
+inline cudaError_t kernel_setup(KernelSetup& k, const void* kernel, size_t smem, int device) {
+  if (k.done[device].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) k.done[device].store(true, std::memory_order_release);
+  return e;
 }
 
 cudaError_t launch_w4_pack(const uint8_t* codes, const __half* scales, const uint8_t* zeros, const W4Weight& w,

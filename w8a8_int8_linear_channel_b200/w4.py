@@ -122,7 +122,8 @@ def sq_w4_pack(codes: torch.Tensor, scales: torch.Tensor, w4: W4Weight, zeros=No
         parts = [(codes[e], scales[e], None if zeros is None else zeros[e], w4[e]) for e in range(w4.experts)]
     for c, s, z, dst in parts:
         if s.data_ptr() % 16 or (z is not None and z.data_ptr() % 16):  # an expert's slice may start off 16 bytes
-            s, z = s.clone(), None if z is None else z.clone()
+            with torch.cuda.stream(stream):  # copied, and the copy's memory reused, in this stream's order
+                s, z = s.clone(), None if z is None else z.clone()
         pc, ps, pz, pw = _ptrs(c, s, z, dst.packed)
         _check(_L.sq_w4_pack(pc, ps, pz, w4.N, w4.K, w4.group, pw, _stream(stream)), "sq_w4_pack")
     return w4
