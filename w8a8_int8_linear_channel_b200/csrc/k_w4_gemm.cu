@@ -109,8 +109,12 @@ struct Layout {
   static constexpr int X_THREADS = 128;  // of the cp.async form
   static constexpr int THREADS = X_WARP * 32 + X_THREADS;
   static constexpr int REC = w4_record_bytes(G, ZERO);
-  static constexpr int XSTAGE = BT * kW4K * 2;             // two boxes of [BT][64 k], 128-byte swizzle
-  static constexpr int XS = BT == 64 || RT == 2 ? 4 : 2;  // token stages
+  // boxes of [BT][64 k] per token stage, 128-byte swizzle (with 128 tokens and half
+  // the memory two stages of two boxes took 29.3 us where four of one take 23.4, 16384 x 4096)
+  static constexpr int XB = BT == 128 && RT == 1 ? 1 : 2;
+  static constexpr int SPT = 2 / XB;                       // token stages per K tile
+  static constexpr int XSTAGE = XB * BT * 128;
+  static constexpr int XS = 4;                            // token stages
   static constexpr int RS = 4;                            // record stages, RT records each
   static constexpr int AS = RT == 2 || BT == 128 ? 2 : 3;  // operand buffers in tensor memory
   static constexpr int D_COLS = RT * BT;
@@ -159,8 +163,9 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   const int slice = blockIdx.x % slices;
   const int block = blockIdx.x / slices % blocks;
   const int tile = blockIdx.x / slices / blocks * RT;  // first weight tile
-  // done: the MMAs of a K tile have run, one barrier per token stage (it frees
-  // the operand buffer too: a buffer's tile is AS <= XS + 1 tiles back)
+  // done: the MMAs of a token stage have run (the last one of a K tile frees the
+  // operand buffer too: a buffer's tile is AS tiles back, and by then the stage
+  // is at most one use further)
   const uint32_t x_full = sbase + L::BARS, done = x_full + 8 * L::XS;
   const uint32_t r_full = done + 8 * L::XS, r_empty = r_full + 8 * L::RS;
   const uint32_t a_full = r_empty + 8 * L::RS, d_full = a_full + 8 * L::AS;
@@ -262,7 +267,8 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(v0[e]), "+r"(v1[e]));  // (not sunk below the wait)
       // the tile that used this buffer before
       const int b = i - L::AS;
-      if (b >= 0 && !w4_wait_warp(done + 8 * (b % L::XS), (b / L::XS) & 1, budget, status, abort)) break;
+      const int bs = b * L::SPT + L::SPT - 1;  // its last stage
+      if (b >= 0 && !w4_wait_warp(done + 8 * (bs % L::XS), (bs / L::XS) & 1, budget, status, abort)) break;
       tc_fence_after();
       tmem_st_x16(col, v0);
       tmem_st_x16(col + 16, v1);
@@ -285,28 +291,31 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     const uint32_t leader = elect_one();
     const uint64_t desc0 = sdesc_k_sw128(sbase + L::X);
     const bool short_tail = p.w.K - static_cast<int64_t>(kt0 + n - 1) * kW4K <= 64;  // one box in the last tile
+    const int steps = 2 * n - (short_tail ? 1 : 0);  // boxes of 64 k
     uint32_t xs = 0, as = 0, xp = 0, ap = 0;
-    bool ready = false;  // the tile's operands were seen to be there while the tile before was being issued
-    for (int i = 0; i < n; ++i) {
+    bool ready = false;  // the stage's operands were seen to be there while the stage before was being issued
+    for (int i = 0; i < steps; i += L::XB) {
       if (!ready) {
-        if (!w4_wait_warp(a_full + 8 * as, ap, budget, status, abort)) break;
+        if ((L::XB == 2 || !(i & 1)) && !w4_wait_warp(a_full + 8 * as, ap, budget, status, abort)) break;
         if (!w4_wait_warp(x_full + 8 * xs, xp, budget, status, abort)) break;
       }
       tc_fence_after();
       if (p.offsets) fence_proxy_async_smem();  // cp.async rows, visible to this thread, to the MMA's reads
       const uint64_t b0 = desc0 + xs * (L::XSTAGE >> 4);
-      const uint32_t a0 = tmem + L::A0 + as * (RT * kACols), mine = done + 8 * xs;
+      const uint32_t a0 = tmem + L::A0 + as * (RT * kACols) + (L::XB == 1 && (i & 1) ? 32 : 0), mine = done + 8 * xs;
       if (++xs == L::XS) xs = 0, xp ^= 1;
-      if (++as == L::AS) as = 0, ap ^= 1;
+      const bool last = L::XB == 2 || (i & 1);  // of the K tile
+      if (last && ++as == L::AS) as = 0, ap ^= 1;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j == 4 && short_tail && i == n - 1) break;  // (the A columns past K are zero, the B rows were not copied)
+      for (int j = 0; j < 4 * L::XB; ++j) {
+        if (j == 4 && i + 1 >= steps) break;  // (the A columns past K are zero, the B rows were not copied)
         const uint64_t b = b0 + (((j >> 2) * BT * 128 + (j & 3) * 32) >> 4);
 #pragma unroll
         for (int t = 0; t < RT; ++t)
           mma_f16_ts(tmem + t * BT, a0 + t * kACols + 8 * j, b, idesc, i > 0 || j > 0, leader);
-        if (j == 6)
-          ready = __all_sync(0xffffffffu, i + 1 < n && mbar_try_wait(a_full + 8 * as, ap) && mbar_try_wait(x_full + 8 * xs, xp));
+        if (j == 4 * L::XB - 2)
+          ready = __all_sync(0xffffffffu, i + L::XB < steps && (!last || mbar_try_wait(a_full + 8 * as, ap)) &&
+                                              mbar_try_wait(x_full + 8 * xs, xp));
       }
       if (leader) mma_commit(mine);
     }
@@ -337,13 +346,15 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     if (warp == L::X_WARP && lane == 0) {
       int issued = 0;
       uint32_t xs = 0, xp = 1;
-      for (int i = 0; i < n; ++i) {
+      for (int i = 0; i < n * L::SPT; ++i) {
+        const int32_t k = kt0 * kW4K + i * (64 * L::XB);
+        // a box of a short last tile may lie past K altogether: it is left
+        // out, and so are its MMAs
+        const int64_t left = p.w.K - k;
+        if (left <= 0) break;
         if (!w4_wait(done + 8 * xs, xp, budget, status, abort)) break;
         const uint32_t stage = sbase + L::X + xs * L::XSTAGE, bar = x_full + 8 * xs;
-        const int32_t k = (kt0 + i) * kW4K;
-        // the second box of a short last tile may lie past K altogether: it is
-        // left out, and so are its MMAs
-        const int boxes = p.w.K - k > 64 ? 2 : 1;
+        const int boxes = L::XB == 2 && left > 64 ? 2 : 1;
         mbar_arrive_expect_tx(bar, boxes * (BT * 128));
         for (int b = 0; b < boxes; ++b) tma_load_2d(stage + b * (BT * 128), &tmX, bar, k + 64 * b, block * BT);
         issued = i + 1;
@@ -354,33 +365,34 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
         mbar_drain(x_full + 8 * (i % L::XS), (i / L::XS) & 1, budget);
     }
   } else {
-    // ---- an expert's token rows: 16 lanes copy a row's 128 k; each thread's
-    // arrival fires when its copies have landed, so the ring fills ahead
+    // ---- an expert's token rows: 16 (8) lanes copy a row's 128 (64) k of a stage; each
+    // thread's arrival fires when its copies have landed, so the ring fills ahead
+    constexpr int LANES = 8 * L::XB, ROWS = L::X_THREADS / LANES;
     const int lt = tid - L::X_WARP * 32;
-    const int c = lt & 15;
-    const uint32_t at = static_cast<uint32_t>(c >> 3) * (BT * 128) + (lt >> 4) * 128 + (((c & 7) ^ ((lt >> 4) & 7)) << 4);
-    const __half* src[BT / 8];  // rows lt / 16 + 8 j: row & 7 does not depend on j
+    const int c = lt & (LANES - 1), r0 = lt / LANES;
+    const uint32_t at = static_cast<uint32_t>(c >> 3) * (BT * 128) + r0 * 128 + (((c & 7) ^ (r0 & 7)) << 4);
+    const __half* src[BT / ROWS];  // rows r0 + ROWS j: row & 7 does not depend on j
     uint32_t live = 0;
 #pragma unroll
-    for (int j = 0; j < BT / 8; ++j) {
-      const int32_t xr = xrow[(lt >> 4) + 8 * j];
+    for (int j = 0; j < BT / ROWS; ++j) {
+      const int32_t xr = xrow[r0 + ROWS * j];
       if (xr >= 0) live |= 1u << j;
       src[j] = p.x + static_cast<int64_t>(xr >= 0 ? xr : 0) * p.ldx + static_cast<int64_t>(kt0) * kW4K + 8 * c;
     }
-    int64_t left = p.w.K - static_cast<int64_t>(kt0) * kW4K - 8 * c;
+    int left = static_cast<int>(p.w.K) - kt0 * kW4K - 8 * c;
     uint32_t xs = 0, xp = 1;
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < n * L::SPT && left + 8 * c > 0; ++i) {
       if (!w4_wait_warp(done + 8 * xs, xp, budget, status, abort)) break;
       const uint32_t dst = sbase + L::X + xs * L::XSTAGE + at;
       const uint32_t mask = left > 0 ? live : 0;  // past K: zeros, and no address is read
 #pragma unroll
-      for (int j = 0; j < BT / 8; ++j) {
-        if (8 * j >= count) break;  // rows that no MMA reads but the last sixteen's rest, whose columns go nowhere
+      for (int j = 0; j < BT / ROWS; ++j) {
+        if (ROWS * j >= count) break;  // rows that no MMA reads but the last sixteen's rest, whose columns go nowhere
         const bool on = mask >> j & 1;
-        cp_async16(dst + j * 1024, on ? src[j] : p.x, on ? 16 : 0);
-        src[j] += kW4K;
+        cp_async16(dst + j * (ROWS * 128), on ? src[j] : p.x, on ? 16 : 0);
+        src[j] += 64 * L::XB;
       }
-      left -= kW4K;
+      left -= 64 * L::XB;
       cp_async_arrive(x_full + 8 * xs);
       if (++xs == L::XS) xs = 0, xp ^= 1;
     }
@@ -566,8 +578,15 @@ cudaError_t launch_w4_gemm(const W4Product& p, const Ctx& c, int64_t tokens) {
   // tokens each, blocks of 16 / 32 / 64 / 128: 273 / 239 / 225 / 231 us a layer, with 20:
   // 376 / 262 / 243 / 239, with 32: 500 / 329 / 270 / 252.
   if (tokens <= (p.offsets ? 16 : 64)) return launch_g<64, 1>(p, c);
-  // two weight tiles per CTA halve the token traffic, if enough CTAs are left
-  if (w4_blocks(p, 128) * ((p.w.nt() + 1) / 2) >= c.num_sms) return launch_g<128, 2>(p, c);
+  // One weight tile per CTA and two CTAs per SM, or two tiles and one CTA, which
+  // halves the token traffic: 2.05 against 1.94 us per 128 x 256 x 4096 and SM
+  // (16384 x 4096 at 2048 tokens 233 and 220 us), for experts, whose rows come
+  // without TMA, 540 and 458 us a layer of 1024 tokens.  But 384 tokens, 192
+  // large CTAs, take 64.2 us and 384 small ones 51.8; and where large CTAs would
+  // not cover the SMs only small ones can be sliced along K.
+  const int64_t blocks = w4_blocks(p, 128), nt = p.w.nt();
+  const int64_t small = (blocks * nt + c.num_sms - 1) / c.num_sms, large = (blocks * ((nt + 1) / 2) + c.num_sms - 1) / c.num_sms;
+  if (blocks * ((nt + 1) / 2) >= c.num_sms && (p.offsets || large * 100 <= small * 53)) return launch_g<128, 2>(p, c);
   return launch_g<128, 1>(p, c);
 }
 

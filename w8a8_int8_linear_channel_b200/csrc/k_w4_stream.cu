@@ -186,21 +186,16 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   const int block = static_cast<int>(cluster_id_x());
   // this lane's token: slot g of the block
-  int expert = 0, count, row = -1;
+  int expert = 0, start = 0, count, row = -1;
   if (p.offsets == nullptr) {
     const int64_t first = static_cast<int64_t>(block) * kTokens;
     count = static_cast<int>(p.M - first < kTokens ? p.M - first : kTokens);
     if (g < count) row = static_cast<int>(first) + g;
   } else {
-    int start = 0;
     expert = w4_find_block(p, block, kTokens, lane, &start, &count);
     if (expert < 0) {  // there is no such block; the same for every CTA of the cluster
       if (slices > 1) cluster_wait();
       return;
-    }
-    if (g < count) {
-      const int32_t pair = p.order[start + g];
-      if (pair >= 0 && pair < p.M) row = pair;
     }
   }
   float acc[2][4];
@@ -211,8 +206,6 @@ __global__ void __launch_bounds__(kThreads, 3)
   {
     const uint8_t* rec =
         p.w.data + ((static_cast<int64_t>(expert) * nt + tile) * KT + kt0 + kg) * static_cast<int64_t>(REC);
-    const int some = row < 0 ? 0 : p.div == 1 ? row : row / p.div;
-    const __half* x = p.x + some * p.ldx + static_cast<int64_t>(kt0 + kg) * kW4K + 8 * t;
     // the CTA's last tile when it is short (its length: tail)
     const int tail = static_cast<int>(p.w.K) & (kW4K - 1);
     const int last = tail && kt0 + n == KT ? n - 1 : -1;
@@ -227,6 +220,13 @@ __global__ void __launch_bounds__(kThreads, 3)
       cp_async_commit();
     }
     rec += (kDepth - 1) * (kKGroups * REC);
+    // (which token: only after the weight's first tiles are on their way)
+    if (p.offsets != nullptr && g < count) {
+      const int32_t pair = p.order[start + g];
+      if (pair >= 0 && pair < p.M) row = pair;
+    }
+    const int some = row < 0 ? 0 : p.div == 1 ? row : row / p.div;
+    const __half* x = p.x + some * p.ldx + static_cast<int64_t>(kt0 + kg) * kW4K + 8 * t;
     int now = 0, ahead = (kDepth - 1) * R::STAGE;  // byte offsets of this tile's stage and of the one to fill
     uint4 xv[4];
 #pragma unroll
