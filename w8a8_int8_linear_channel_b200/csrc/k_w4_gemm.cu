@@ -506,9 +506,10 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   if (warp == L::MMA_WARP) tmem_dealloc(tmem, L::TMEM_COLS);
 }
 
-// Slices of K per weight tile (the cluster size).  A CTA's time is taken as 0.39 us per K tile and 64
-// tokens, 4.5 for start and finish and 4 more for the cluster's sum (4096 x
-// 4096 at 64 tokens: 17.0 us with one slice, 11.5 with four).  Two CTAs on an
+// Slices of K per weight tile (the cluster size).  A CTA's time is taken as
+// 0.39 us per K tile (0.59 with 128 tokens), 4.5 for start and finish and 4
+// more for the cluster's sum (4096 x 4096 at 64 tokens: 17.0 us with one slice,
+// 11.5 with four).  Two CTAs on an
 // SM overlap their tiles, hardly the rest: with clusters until every SM has
 // two, 4096 x 4096 at 384 tokens took 41.1 us, with one slice 26.4.  Clusters
 // of more than two do not pack every SM of a GPC; an eighth is taken off
@@ -519,7 +520,7 @@ int pick_slices(int64_t units, int64_t kt, int bt, int num_sms) {
   for (int s = 1; s <= kMaxSlices && (s == 1 || kt / s >= 4); ++s) {
     const int64_t sms = s <= 2 ? num_sms : num_sms - num_sms / 8;
     const int64_t per_sm = (units * s + sms - 1) / sms;
-    const int64_t cost = (per_sm + 1) / 2 * ((kt + s - 1) / s) * (bt / 64) * 39 + per_sm * (s == 1 ? 450 : 850);
+    const int64_t cost = (per_sm + 1) / 2 * ((kt + s - 1) / s) * (bt == 64 ? 39 : 59) + per_sm * (s == 1 ? 450 : 850);
     if (cost < best) best = cost, slices = s;
   }
   return slices;
@@ -585,8 +586,9 @@ cudaError_t launch_w4_gemm(const W4Product& p, const Ctx& c, int64_t tokens) {
   // large CTAs, take 64.2 us and 384 small ones 51.8; and where large CTAs would
   // not cover the SMs only small ones can be sliced along K.
   const int64_t blocks = w4_blocks(p, 128), nt = p.w.nt();
-  const int64_t small = (blocks * nt + c.num_sms - 1) / c.num_sms, large = (blocks * ((nt + 1) / 2) + c.num_sms - 1) / c.num_sms;
-  if (blocks * ((nt + 1) / 2) >= c.num_sms && (p.offsets || large * 100 <= small * 53)) return launch_g<128, 2>(p, c);
+  const int64_t pairs = blocks * ((nt + 1) / 2);
+  const int64_t small = (blocks * nt + c.num_sms - 1) / c.num_sms, large = (pairs + c.num_sms - 1) / c.num_sms;
+  if (pairs >= c.num_sms && (p.offsets || large * 100 <= small * 53)) return launch_g<128, 2>(p, c);
   return launch_g<128, 1>(p, c);
 }
 
