@@ -1,6 +1,6 @@
-// k_w4_stream.cu -- y = x W^T with a packed 4-bit W for up to eight tokens per
-// weight tile: the weight is streamed once, and everything else is arranged
-// around that stream.
+// k_w4_stream.cu -- y = x W^T with a packed 4-bit W for few tokens: the weight
+// is streamed once per eight tokens, and everything else is arranged around
+// that stream.
 //
 //   y[m, n] = fp16( sum_g s[n, g] * sum_{k in g} (q[n, k] - z[n, g]) x[m, k] + bias[n] )
 //
@@ -9,17 +9,20 @@
 // 8-column one (fp32 accumulators); a group's sum is multiplied by its scale
 // once, in fp32, so no weight is ever rounded.
 //
-// Every warp is a stream of its own: it owns 32 channels and every fourth K
-// tile of its CTA's slice, loads a tile's codes (2 KB, contiguous) and scales
-// straight into registers while it computes on the tile before, and shares
-// nothing with other warps until the end.  The arithmetic is what bounds this kernel (about 185 warp
-// instructions per 32 channels x 128 k, and the memory's rate leaves 350 cycles
-// per SM for four times that), so it must not wait or synchronize: with the
-// same arithmetic behind a ring of bulk copies in shared memory, 100 more
-// instructions per tile went into barriers and the producer.
+// Every warp is a stream of its own: it owns 32 channels and every second or
+// fourth K tile of its CTA's slice, copies a tile's codes (2 KB, contiguous) and
+// scales into a ring of its own in shared memory two tiles ahead, and shares
+// nothing with other warps until the end: a lane reads back the codes that it
+// copied itself.  With the same arithmetic behind a ring of bulk copies for the
+// whole CTA, 100 more instructions per tile went into barriers and the producer.
 //
-// A CTA owns half a 128-channel tile and a slice of K; the CTAs of a cluster own
-// the slices of one half.  At the end every warp pushes its sums to the CTA of
+// What bounds it is the issue of instructions: 271 per 32 channels x 128 k with
+// everything, 181 of them arithmetic.  49152 x 12288 at one token takes 64.6 us
+// = 4.8 TB/s (0.74 of the copy bandwidth; 47.9 us without the arithmetic), its
+// schedulers 68% busy; 4096 x 4096 takes 5.0 us, most of it start and finish.
+//
+// A CTA owns 64 or 128 channels and a slice of K; the CTAs of a cluster own the
+// slices of the same channels.  At the end every warp pushes its sums to the CTA of
 // the cluster that finishes those channels (distributed shared memory), which
 // adds them in a fixed order: no atomics, no workspace, the same bits on every
 // run.
@@ -163,15 +166,15 @@ __device__ __forceinline__ void consume(const uint8_t* stage, int lane, uint4 (&
 // kRowGroups warps along the channels, 32 each, and the others along K.
 template <int kRowGroups, int G, bool ZERO>
 __global__ void __launch_bounds__(kThreads, 3)
-    k_w4_stream(const W4Product p, int slices, int KT, int nt, uint32_t share_inv) {
+    k_w4_stream(const W4Product p, int slices, int KT, int nt, int share_shift) {
   constexpr int kKGroups = kWarps / kRowGroups;
   constexpr int kRows = kRowGroups * 32, kParts = kW4Rows / kRows;  // channels per CTA, CTAs per weight tile
   using R = Ring<G, ZERO>;
   constexpr int REC = w4_record_bytes(G, ZERO);
   // sums of every slice and K group for the channels this CTA finishes:
-  // [slices * kKGroups][channels per CTA][kTokens]
+  // [slices * kKGroups][kRows / slices][kTokens]
   extern __shared__ __align__(128) uint8_t smem[];  // every warp's ring
-  __shared__ __align__(16) float red[kKGroups * (kRows + kMaxSlices) * kTokens];
+  __shared__ __align__(16) float red[kKGroups * kRows * kTokens];
   const int lane = threadIdx.x & 31;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int slice = static_cast<int>(cluster_ctarank());
@@ -254,14 +257,14 @@ __global__ void __launch_bounds__(kThreads, 3)
   griddep_launch_dependents();
 
   // push the sums to the CTAs that finish these channels
-  const int share = (kRows + slices - 1) / slices;  // channels each CTA of the cluster finishes
+  const int share = 1 << share_shift;  // channels each CTA of the cluster finishes: kRows / slices
   if (slices > 1) cluster_wait();
   const uint32_t src = (slice * kKGroups + kg) * share;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int r = r0 + 8 * j;
-    const int owner = static_cast<int>(r * share_inv >> 16);  // r / share
-    const uint32_t at = (src + r - owner * share) * kTokens + 2 * t;
+    const int owner = r >> share_shift;
+    const uint32_t at = (src + (r & (share - 1))) * kTokens + 2 * t;
     const float a = acc[j >> 1][2 * (j & 1)], b = acc[j >> 1][2 * (j & 1) + 1];
     if (slices > 1)
       st_cluster_v2(mapa_shared(smem_u32(red + at), owner), a, b);
@@ -295,14 +298,24 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
 }
 
-// Slices of K (the cluster size): as many as give every SM one CTA, a K tile
-// per warp at least.  More would share SMs and pay for larger clusters: 4096 x 4096 at
-// one token takes 6.6 / 5.0 / 6.2 us with 1 / 2 / 4 slices, 4096 x 16384 19.5 /
-// 12.0 / 12.4, 16384 x 4096 (256 CTAs already) 12.0 / 14.0 / 17.2.
+// Slices of K (the cluster size, a power of two, so that the CTAs finish as many
+// channels each), a K tile per warp at least: the fewest that give the shortest
+// busiest SM.  CTAs on one SM share its issue slots, so their tiles add up (one
+// CTA alone cannot fill them: it takes the time of one and a half); each
+// costs 16 tiles' worth besides.  Clusters of more than two do not pack every
+// SM.  With 1 / 2 / 4 slices 4096 x 4096 at one token takes 6.5 / 5.0 / 6.0 us, 8192 x
+// 8192 13.9 / 12.0 / 14.6, 16384 x 4096 11.8 / 13.4 / 17.1, 12288 x 49152 (192
+// CTAs) 85.1 / 65.5 / 67.2.
 int pick_slices(int64_t ctas, int64_t kt, int k_groups, int num_sms) {
-  int64_t s = num_sms / ctas;
-  if (s > kt / k_groups) s = kt / k_groups;
-  return s < 1 ? 1 : s > kMaxSlices ? kMaxSlices : static_cast<int>(s);
+  int slices = 1;
+  int64_t best = INT64_MAX;
+  for (int s = 1; s <= kMaxSlices && (s == 1 || s <= kt / k_groups); s *= 2) {
+    const int64_t sms = s <= 2 ? num_sms : num_sms - num_sms / 8;
+    const int64_t n = (ctas * s + sms - 1) / sms, tiles = (kt + s - 1) / s;
+    const int64_t cost = (n == 1 ? 3 : 2 * n) * tiles + 32 * n;
+    if (cost < best) best = cost, slices = s;
+  }
+  return slices;
 }
 
 template <int kRowGroups, int G, bool ZERO>
@@ -318,8 +331,9 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   // (experts: about a block each, if there are that many pairs)
   const int64_t likely = !p.offsets ? blocks : p.M < p.E ? p.M : p.E;
   const int slices = pick_slices(units * likely, kt, kKGroups, c.num_sms);
-  // ceil(2^16 / share): r * share_inv >> 16 is r / share for every channel r of the CTA
-  const uint32_t share = (kRows + slices - 1) / slices, share_inv = (65536 + share - 1) / share;
+  int share_shift = kRowGroups == 2 ? 6 : 7;
+  for (int s = slices; s > 1; s >>= 1) --share_shift;
+  static_assert(kRows == (kRowGroups == 2 ? 64 : 128), "channels per CTA");
   static_assert(kRowGroups < 4 || SQ_W4_MAX_N <= 65535LL * kRows, "grid.y");
   if (units > 65535 || blocks * slices > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
@@ -336,7 +350,7 @@ cudaError_t launch(const W4Product& p, const Ctx& c) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, slices, static_cast<int>(kt), static_cast<int>(nt), share_inv);
+  return cudaLaunchKernelEx(&cfg, kernel, p, slices, static_cast<int>(kt), static_cast<int>(nt), share_shift);
 }
 
 template <int kRowGroups>

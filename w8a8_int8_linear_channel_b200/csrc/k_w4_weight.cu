@@ -1,10 +1,12 @@
 // k_w4_weight.cu -- making and reading packed 4-bit weights: quantization of
 // an fp16 weight in groups, packing of codes a caller already has, and the
-// fp16 values of a packed weight.  All three are bound by HBM when they are
+// fp16 values of a packed weight.  They come near the rate of HBM when they are
 // written so that nothing but the eight values of a packed word is computed
 // per thread: a warp takes two channels (the quantizer four), lane l the k =
 // 8 l .. 8 l + 7 of a tile (one 16-byte load or store, one packed word), and
-// walks along K with the next tile's load in flight.
+// walks along K with the next tile's load in flight.  16384 x 4096 with a fold:
+// quantize 41 us (169 MB at 4.1 TB/s, 0.64 of the copy bandwidth; its schedulers
+// are 78% busy), dequantize 32.5 us (5.2 TB/s, 0.81).
 #include "sq_w4.cuh"
 
 namespace sq {
