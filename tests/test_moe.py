@@ -418,3 +418,53 @@ def test_layer_captured_and_on_two_streams(cuda_device):
                     g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(y, w) for (_, y), w in zip(graphs, want))
+
+
+# ----------------------------------------------------------------- guard bands ----
+class _Guard:
+    """Tensors between margins of a byte pattern that every call has to leave alone."""
+    MARGIN = 4096
+
+    def __init__(self):
+        self.buffers = []
+
+    def __call__(self, shape, dtype):
+        n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((n + 2 * self.MARGIN,), 0x5A, dtype=torch.uint8, device="cuda")
+        self.buffers.append((buf, n))
+        return buf[self.MARGIN:self.MARGIN + n].view(dtype).view(shape)
+
+    def check(self):
+        for buf, n in self.buffers:
+            assert bool((buf[:self.MARGIN] == 0x5A).all()) and bool((buf[self.MARGIN + n:] == 0x5A).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,topk,K,F,group", [(1, 5, 2, 48, 72, 32), (37, 6, 3, 272, 136, 64), (300, 4, 2, 144, 400, 128),
+                                                (700, 3, 2, 1040, 4000, 128)])
+def test_outputs_inside_guard_bands(cuda_device, T, E, topk, K, F, group):
+    import w8a8_int8_linear_channel_b200 as sq
+    rng = np.random.default_rng(T)
+    g, P = _Guard(), T * topk
+    w = dev((rng.standard_normal((E, F, K)) * 0.05).astype(np.float16))
+    w4 = sq.W4Weight(g((sq.sq_w4_packed_bytes(F, K, group, True) * E,), torch.uint8), F, K, group, True, E)
+    sq.sq_quantize_weight_w4(w, w4)
+    back = g((F, K), torch.float16)
+    sq.sq_w4_dequantize(w4[E - 1], back)
+    step = float(w.float().abs().max()) / 15 * 2
+    assert float((back.float() - w[E - 1].float()).abs().max()) <= step
+    x = dev(_tokens(rng, T, K))
+    ids, wt = g((T, topk), torch.int32), g((T, topk), torch.float32)
+    sq.sq_moe_route(dev(rng.standard_normal((T, E)).astype(np.float32)), ids, wt)
+    off, order = g((E + 1,), torch.int32), g((P,), torch.int32)
+    need = sq.sq_moe_plan_workspace_bytes(P, E)
+    sq.sq_moe_plan(ids, off, order, workspace=g((need,), torch.uint8) if need else None)
+    for dtype in (torch.float16, torch.float32):
+        y = g((P, F), dtype)
+        sq.sq_w4a16_experts(x, w4, off, order, y, topk)
+        out = g((T, F), torch.float16)
+        sq.sq_moe_combine(y, ids, wt, E, out)
+        assert bool(torch.isfinite(out).all())
+    torch.cuda.synchronize()
+    assert sq.sq_poll_status() == 0
+    g.check()
