@@ -22,7 +22,8 @@ GROUPS = (32, 64, 128)
 # These calls take a few microseconds on the GPU, so their host side counts: one
 # look at the current device per call, plain integers as pointers, and the
 # current stream's handle without a Stream object where torch offers it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _F16, _F32, _I32 = torch.float16, torch.float32, torch.int32
 
@@ -42,11 +43,7 @@ def _ptrs(*tensors):
 
 
 def _stream(stream) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(_current_device())
-    return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_current_device()) if stream is None else stream.cuda_stream
 
 
 class W4Weight:
@@ -157,8 +154,14 @@ def sq_w4a16_linear(x: torch.Tensor, w4: W4Weight, y: torch.Tensor, bias=None, r
         _tensor(y, _F16, (M, N), "y")
     if bias is not None:
         _vec(bias, N, _F16, "bias")
-    px, pw, py, pb = _ptrs(x, w4.packed, y, bias)
-    status = _L.sq_w4a16_linear(px, M, ld, pw, N, K, w4.group, w4.zero_point, pb, bool(relu), py, _stream(stream))
+    packed = w4.packed
+    dev = x.get_device()
+    if dev < 0 or dev != packed.get_device() or dev != y.get_device() or (
+            bias is not None and dev != bias.get_device()) or dev != _current_device():
+        _ptrs(x, packed, y, bias)  # says what is wrong
+    status = _L.sq_w4a16_linear(x.data_ptr(), M, ld, packed.data_ptr(), N, K, w4.group, w4.zero_point,
+                                None if bias is None else bias.data_ptr(), bool(relu), y.data_ptr(),
+                                _raw_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         _check(status, "sq_w4a16_linear")
     return y
@@ -177,18 +180,29 @@ def sq_moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
         raise ValueError("logits: fp32 or fp16")
     if score not in _SCORES:
         raise ValueError(f"score: one of {sorted(_SCORES)}")
-    T, E, ld = _rows(logits, logits.dtype, "logits")
+    if logits.dim() != 2:
+        _rows(logits, logits.dtype, "logits")
+    T, E = logits.shape
+    ld, inner = logits.stride()
+    if inner != 1:
+        _rows(logits, logits.dtype, "logits")
     shape = ids.shape
     if len(shape) != 2 or shape[0] != T:
         raise ValueError(f"ids: need [{T}, topk]")
-    topk = shape[1]
-    _tensor(ids, _I32, shape, "ids")
-    _tensor(weights, _F32, shape, "weights")
+    if ids.dtype != _I32 or not ids.is_contiguous():
+        _tensor(ids, _I32, shape, "ids")
+    if weights.dtype != _F32 or weights.shape != shape or not weights.is_contiguous():
+        _tensor(weights, _F32, shape, "weights")
     if bias is not None:
         _vec(bias, E, _F32, "bias")
-    pl, pi, pw, pb = _ptrs(logits, ids, weights, bias)
-    status = _L.sq_moe_route(pl, half, T, E, max(ld, E) if T == 1 else ld, pb, _SCORES[score], n_group, topk_group,
-                             group_top, topk, bool(renormalize), scale, pi, pw, _stream(stream))
+    dev = logits.get_device()
+    if dev < 0 or dev != ids.get_device() or dev != weights.get_device() or (
+            bias is not None and dev != bias.get_device()) or dev != _current_device():
+        _ptrs(logits, ids, weights, bias)  # says what is wrong
+    status = _L.sq_moe_route(logits.data_ptr(), half, T, E, E if T == 1 else ld,
+                             None if bias is None else bias.data_ptr(), _SCORES[score], n_group, topk_group,
+                             group_top, shape[1], bool(renormalize), scale, ids.data_ptr(), weights.data_ptr(),
+                             _raw_stream(dev) if stream is None else stream.cuda_stream)
     if status:
         _check(status, "sq_moe_route")
     return ids, weights
@@ -202,18 +216,27 @@ def sq_moe_plan(ids: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor, w
     """The (token, slot) pairs of ids (int32, any shape) stably sorted by expert: offsets int32
     [E + 1], order int32 [ids.numel()].  Without a workspace one is allocated for the call."""
     pairs, E = ids.numel(), offsets.numel() - 1
-    if ids.dtype != torch.int32 or not ids.is_contiguous():
+    if ids.dtype != _I32 or not ids.is_contiguous():
         raise ValueError("ids: need a contiguous int32 tensor")
-    _vec(offsets, E + 1, torch.int32, "offsets")
-    _vec(order, pairs, torch.int32, "order")
+    if offsets.dtype != _I32 or not offsets.is_contiguous():
+        _vec(offsets, E + 1, _I32, "offsets")
+    if order.dtype != _I32 or order.numel() != pairs or not order.is_contiguous():
+        _vec(order, pairs, _I32, "order")
     if workspace is None:
-        need = sq_moe_plan_workspace_bytes(pairs, E)
+        need = int(_L.sq_moe_plan_workspace_bytes(pairs, E))
         if need:
             with torch.cuda.stream(stream):  # freed memory is reused in this stream's order
                 workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    pi, pf, po, pw = _ptrs(ids, offsets, order, workspace)
-    _check(_L.sq_moe_plan(pi, pairs, E, pf, po, pw, ws_bytes, _stream(stream)), "sq_moe_plan")
+    dev = ids.get_device()
+    if dev < 0 or dev != offsets.get_device() or dev != order.get_device() or (
+            workspace is not None and dev != workspace.get_device()) or dev != _current_device():
+        _ptrs(ids, offsets, order, workspace)  # says what is wrong
+    status = _L.sq_moe_plan(ids.data_ptr(), pairs, E, offsets.data_ptr(), order.data_ptr(),
+                            None if workspace is None else workspace.data_ptr(), ws_bytes,
+                            _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status, "sq_moe_plan")
     return offsets, order
 
 
@@ -286,7 +309,7 @@ class W4Linear:
         lead = tuple(x.shape[:-1])
         x2 = x if x.dim() == 2 else x.reshape(-1, K)
         if y is None:
-            y = torch.empty(lead + (N,), dtype=torch.float16, device=x.device)
+            y = x.new_empty(lead + (N,), dtype=_F16)
         elif tuple(y.shape) not in (lead + (N,), (x2.shape[0], N)) or not y.is_contiguous():
             raise ValueError(f"y: need a contiguous fp16 {lead + (N,)} tensor")
         if x2.shape[0]:
@@ -331,42 +354,55 @@ class W4Experts:
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         """x fp16 [..., K] and router logits [..., E] (fp32 or fp16) -> y fp16 [..., K]."""
-        E, F, K = self.up.experts, self.up.N, self.up.K
-        if x.dim() < 1 or x.shape[-1] != K or tuple(logits.shape) != tuple(x.shape[:-1]) + (E,):
-            raise ValueError(f"x / logits: need [..., {K}] and [..., {E}], got {tuple(x.shape)}, {tuple(logits.shape)}")
-        if x.dtype != torch.float16 or logits.dtype not in (torch.float32, torch.float16):
+        up, down, topk = self.up, self.down, self.topk
+        E, F, K = up.experts, up.N, up.K
+        shape, lshape = x.shape, logits.shape
+        if not shape or shape[-1] != K or lshape[-1:] != (E,) or lshape[:-1] != shape[:-1]:
+            raise ValueError(f"x / logits: need [..., {K}] and [..., {E}], got {tuple(shape)}, {tuple(lshape)}")
+        half = logits.dtype == _F16
+        if x.dtype != _F16 or not (half or logits.dtype == _F32):
             raise ValueError("x: fp16; logits: fp32 or fp16")
-        x2, l2 = x.reshape(-1, K), logits.reshape(-1, E)
-        if x2.stride(1) != 1 or l2.stride(1) != 1:
+        x2, l2 = (x, logits) if len(shape) == 2 else (x.reshape(-1, K), logits.reshape(-1, E))
+        (T, _), (ldx, inner), (ldl, linner) = x2.shape, x2.stride(), l2.stride()
+        if inner != 1 or linner != 1:
             raise ValueError("x / logits: need a unit inner stride")
-        T = x2.shape[0]
-        P = T * self.topk
-        y = torch.empty(x.shape, dtype=torch.float16, device=x.device)
+        y = x.new_empty(shape)
         if T == 0:
             return y
+        if T == 1:
+            ldx, ldl = K, E  # the stride of a single row means nothing
+        P = T * topk
         # The whole layer is a few tens of microseconds for a few tokens, so the calls below pass
         # addresses inside one allocation instead of tensors cut from it.
-        up, down, topk = self.up, self.down, self.topk
-        plan_ws = sq_moe_plan_workspace_bytes(P, E)
+        plan_ws = _L.sq_moe_plan_workspace_bytes(P, E)
         at, end = [], 0
         for n in (4 * P, 4 * P, 4 * (E + 1), 4 * P, plan_ws, 2 * P * F, 4 * P * K):
             at.append(end)
             end += -(-n // 256) * 256
-        buf = torch.empty(end, dtype=torch.uint8, device=x.device)
+        buf = x.new_empty(end // 2)
         px, pl, prb, pu, pub, pd, pdb, pbuf, py = _ptrs(x2, l2, self.router_bias, up.packed, self.up_bias, down.packed,
                                                         self.down_bias, buf, y)
-        ids, weights, offsets, order, ws, h, z = (pbuf + a for a in at)
-        st = _stream(None)
-        _check(_L.sq_moe_route(pl, logits.dtype == torch.float16, T, E, l2.stride(0) if T > 1 else E, prb,
-                               _SCORES[self.score], self.n_group, self.topk_group, self.group_top, topk,
-                               self.renormalize, self.scale, ids, weights, st), "sq_moe_route")
-        _check(_L.sq_moe_plan(ids, P, E, offsets, order, ws, plan_ws, st), "sq_moe_plan")
-        _check(_L.sq_w4a16_experts(px, T, x2.stride(0) if T > 1 else K, pu, E, F, K, up.group, up.zero_point, pub, True,
-                                   offsets, order, P, topk, h, False, st), "sq_w4a16_experts")
+        ids, weights, offsets, order, ws, h, z = [pbuf + a for a in at]
+        st = _raw_stream(x2.get_device())
+        status = _L.sq_moe_route(pl, half, T, E, ldl, prb, _SCORES[self.score], self.n_group, self.topk_group,
+                                 self.group_top, topk, self.renormalize, self.scale, ids, weights, st)
+        if status:
+            _check(status, "sq_moe_route")
+        status = _L.sq_moe_plan(ids, P, E, offsets, order, ws, plan_ws, st)
+        if status:
+            _check(status, "sq_moe_plan")
+        status = _L.sq_w4a16_experts(px, T, ldx, pu, E, F, K, up.group, up.zero_point, pub, True, offsets, order, P,
+                                     topk, h, False, st)
+        if status:
+            _check(status, "sq_w4a16_experts")
         # fp32 rows, so that the layer's output is rounded once
-        _check(_L.sq_w4a16_experts(h, P, F, pd, E, K, F, down.group, down.zero_point, pdb, False, offsets, order, P, 1,
-                                   z, True, st), "sq_w4a16_experts")
-        _check(_L.sq_moe_combine(z, True, ids, weights, T, topk, K, E, py, st), "sq_moe_combine")
+        status = _L.sq_w4a16_experts(h, P, F, pd, E, K, F, down.group, down.zero_point, pdb, False, offsets, order, P,
+                                     1, z, True, st)
+        if status:
+            _check(status, "sq_w4a16_experts")
+        status = _L.sq_moe_combine(z, True, ids, weights, T, topk, K, E, py, st)
+        if status:
+            _check(status, "sq_moe_combine")
         return y
 
     __call__ = forward
