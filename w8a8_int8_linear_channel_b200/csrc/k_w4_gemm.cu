@@ -137,8 +137,8 @@ struct Layout {
   static constexpr int NBARS = 2 * XS + 2 * RS + AS + 1;
   static constexpr int XROW = BARS + (NBARS * 8 + 15) / 16 * 16;  // int32 [BT]: x row of every token, -1 none
   static constexpr int YROW = XROW + BT * 4;                      // int32 [BT]: y row, -1 none
-  static constexpr int MISC = YROW + BT * 4;                      // abort, TMEM address, expert, count
-  static constexpr int BYTES = MISC + 16 + 1024;                  // alignment slack
+  static constexpr int MISC = YROW + BT * 4;                      // abort, TMEM address, expert, count, first token
+  static constexpr int BYTES = MISC + 32 + 1024;                  // alignment slack
   static_assert(D_COLS + AS * RT * kACols <= TMEM_COLS, "tensor memory");
   // The parity of a barrier's phase tells two successive uses of a stage
   // apart, not three.  A group of warps (K tiles of one parity) that asks for
@@ -178,46 +178,56 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   const uint32_t r_full = done + 8 * L::XS, r_empty = r_full + 8 * L::RS;
   const uint32_t a_full = r_empty + 8 * L::RS, d_full = a_full + 8 * L::AS;
 
-  if (tid == 0) {
-    for (int s = 0; s < L::XS; ++s) mbar_init(x_full + 8 * s, p.offsets ? L::X_THREADS : 1), mbar_init(done + 8 * s, 1);
-    for (int s = 0; s < L::RS; ++s) {
-      mbar_init(r_full + 8 * s, 1);
-      mbar_init(r_empty + 8 * s, RT == 2 ? 8 : 4);
+  const int kt0 = static_cast<int>(static_cast<int64_t>(KT) * slice / slices);
+  const int n = static_cast<int>(static_cast<int64_t>(KT) * (slice + 1) / slices) - kt0;
+  const int64_t nt = p.w.nt();
+
+  // Until the first MMA a CTA waits for three latencies in a row (which expert,
+  // its records, the operand made of them); what can go beside them does:
+  // one warp sets up the barriers, finds the tokens and sends for the first
+  // records before anyone else knows of them, while another takes tensor memory.
+  // (records of K tiles [from, to); returns how many were sent for)
+  auto load_records = [&](int expert, int from, int to) {
+    for (int i = from; i < to; ++i) {
+      const uint32_t rs = i % L::RS;
+      if (!w4_wait(r_empty + 8 * rs, i / L::RS & 1 ^ 1, budget, status, abort)) return i;
+      // the last weight tile may stand alone: its place is taken by itself
+      // again, and nothing of the copy is written out
+      mbar_arrive_expect_tx(r_full + 8 * rs, RT * L::REC);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const int64_t wt = tile + t < nt ? tile + t : nt - 1;
+        bulk_load(sbase + L::R + (rs * RT + t) * L::REC,
+                  p.w.data + ((static_cast<int64_t>(expert) * nt + wt) * KT + kt0 + i) * L::REC, L::REC, r_full + 8 * rs);
+      }
     }
-    for (int s = 0; s < L::AS; ++s) mbar_init(a_full + 8 * s, RT == 2 ? 8 : 4);
-    mbar_init(d_full, 1);
-    *abort = 0;
+    return to;
+  };
+  const int early = n < L::RS ? n : L::RS;
+  if (warp == L::REC_WARP) {
+    for (int i = lane; i < L::NBARS; i += 32) {
+      uint32_t arrivals = 1;
+      if (i < L::XS) arrivals = p.offsets ? L::X_THREADS : 1;                             // x_full
+      if (i >= 2 * L::XS + L::RS && i < L::NBARS - 1) arrivals = RT == 2 ? 8 : 4;       // r_empty, a_full
+      mbar_init(sbase + L::BARS + 8 * i, arrivals);
+    }
+    if (lane == 0) *abort = 0;
     fence_barrier_init();
+    __syncwarp();
   }
   griddep_wait();
-
-  // the block's tokens, found before tensor memory is taken: a block that does
-  // not exist leaves at once
-  if (warp == 0) {
-    int expert = 0, start = 0, count = 0;
-    if (p.offsets == nullptr) {
-      const int64_t first = static_cast<int64_t>(block) * BT;
-      start = static_cast<int>(first);
-      count = static_cast<int>(p.M - first < BT ? p.M - first : BT);
-    } else {
+  if (warp == L::REC_WARP) {
+    int expert = 0, start = block * BT, count = BT;
+    if (p.offsets == nullptr)
+      count = static_cast<int>(p.M - start < BT ? p.M - start : BT);
+    else
       expert = w4_find_block(p, block, BT, lane, &start, &count);
+    if (lane == 0) {
+      misc[2] = expert, misc[3] = count, misc[4] = start;
+      if (expert >= 0) load_records(expert, 0, early);
     }
-    if (lane == 0) misc[2] = expert, misc[3] = count;
-    for (int i = lane; i < BT; i += 32) {
-      int32_t row = -1;
-      if (expert >= 0 && i < count) {
-        row = p.offsets ? p.order[start + i] : start + i;
-        if (row < 0 || row >= p.M) row = -1;
-      }
-      yrow[i] = row;
-      xrow[i] = row < 0 ? -1 : row / p.div;
-    }
-  }
-  __syncthreads();
-  const int expert = misc[2], count = misc[3];
-  if (expert < 0) return;  // the same for every CTA of the cluster
-  if (warp == L::MMA_WARP) {
     __syncwarp();
+  } else if (warp == L::MMA_WARP) {
     tmem_alloc(smem_u32(misc + 1), L::TMEM_COLS);
     tmem_relinquish();
   }
@@ -225,10 +235,11 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[1]);
-
-  const int kt0 = static_cast<int>(static_cast<int64_t>(KT) * slice / slices);
-  const int n = static_cast<int>(static_cast<int64_t>(KT) * (slice + 1) / slices) - kt0;
-  const int64_t nt = p.w.nt();
+  const int expert = misc[2], count = misc[3];
+  if (expert < 0) {  // there is no such block; the same for every CTA of the cluster
+    if (warp == L::MMA_WARP) tmem_dealloc(tmem, L::TMEM_COLS);
+    return;
+  }
 
   if (warp < L::DEQ) {
     // ---- dequantization: thread = channel; a group of four warps takes weight
@@ -330,26 +341,12 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     if (leader) mma_commit(d_full);  // also after a wait that ran out: nothing in flight is left behind
   } else if (warp == L::REC_WARP) {
     // ---- record producer
-    int issued = 0;
-    uint32_t rs = 0, rp = 1;
-    for (int i = 0; i < n && lane == 0; ++i) {
-      if (!w4_wait(r_empty + 8 * rs, rp, budget, status, abort)) break;
-      // the last weight tile may stand alone: its place is taken by itself
-      // again, and nothing of the copy is written out
-      mbar_arrive_expect_tx(r_full + 8 * rs, RT * L::REC);
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const int64_t wt = tile + t < nt ? tile + t : nt - 1;
-        bulk_load(sbase + L::R + (rs * RT + t) * L::REC,
-                  p.w.data + ((static_cast<int64_t>(expert) * nt + wt) * KT + kt0 + i) * L::REC, L::REC, r_full + 8 * rs);
-      }
-      issued = i + 1;
-      if (++rs == L::RS) rs = 0, rp ^= 1;
-    }
+    const int issued = lane == 0 ? load_records(expert, early, n) : 0;
     // records in flight land before the CTA can leave (at once unless a wait ran out)
     for (int i = max(0, issued - L::RS); i < issued; ++i)
       mbar_drain(r_full + 8 * (i % L::RS), (i / L::RS) & 1, budget);
   } else if (p.offsets == nullptr) {
+    for (int i = tid - L::X_WARP * 32; i < BT; i += L::X_THREADS) yrow[i] = i < count ? misc[4] + i : -1;
     // ---- token rows of one matrix: TMA; rows past M and k past K read as zero
     if (warp == L::X_WARP && lane == 0) {
       int issued = 0;
@@ -377,6 +374,13 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     // thread's arrival fires when its copies have landed, so the ring fills ahead
     constexpr int LANES = 8 * L::XB, ROWS = L::X_THREADS / LANES;
     const int lt = tid - L::X_WARP * 32;
+    for (int i = lt; i < BT; i += L::X_THREADS) {
+      int32_t row = i < count ? p.order[misc[4] + i] : -1;
+      if (row < 0 || row >= p.M) row = -1;
+      yrow[i] = row;
+      xrow[i] = row < 0 ? -1 : p.div == 1 ? row : row / p.div;
+    }
+    named_bar_sync(1, L::X_THREADS);
     const int c = lt & (LANES - 1), r0 = lt / LANES;
     const uint32_t at = static_cast<uint32_t>(c >> 3) * (BT * 128) + r0 * 128 + (((c & 7) ^ (r0 & 7)) << 4);
     const __half* src[BT / ROWS];  // rows r0 + ROWS j: row & 7 does not depend on j
@@ -407,6 +411,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     cp_async_wait_all();
   }
   __syncwarp();
+  __syncthreads();  // yrow
 
   // ---- epilogue
   mbar_wait_bounded(d_full, 0, budget > 100000000ull ? budget : 100000000ull);
