@@ -137,8 +137,8 @@ struct Layout {
   static constexpr int NBARS = 2 * XS + 2 * RS + AS + 1;
   static constexpr int XROW = BARS + (NBARS * 8 + 15) / 16 * 16;  // int32 [BT]: x row of every token, -1 none
   static constexpr int YROW = XROW + BT * 4;                      // int32 [BT]: y row, -1 none
-  static constexpr int MISC = YROW + BT * 4;                      // abort, TMEM address, expert, count, first token
-  static constexpr int BYTES = MISC + 32 + 1024;                  // alignment slack
+  static constexpr int MISC = YROW + BT * 4;                      // abort, TMEM address, expert, count
+  static constexpr int BYTES = MISC + 16 + 1024;                  // alignment slack
   static_assert(D_COLS + AS * RT * kACols <= TMEM_COLS, "tensor memory");
   // The parity of a barrier's phase tells two successive uses of a stage
   // apart, not three.  A group of warps (K tiles of one parity) that asks for
@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
 
   // Until the first MMA a CTA waits for three latencies in a row (which expert,
   // its records, the operand made of them); what can go beside them does:
-  // one warp sets up the barriers, finds the tokens and sends for the first
-  // records before anyone else knows of them, while another takes tensor memory.
+  // one warp sets up the barriers, finds the block and sends for its first
+  // records, while another takes tensor memory and the last ones look up the rows.
   // (records of K tiles [from, to); returns how many were sent for)
   auto load_records = [&](int expert, int from, int to) {
     for (int i = from; i < to; ++i) {
@@ -215,6 +215,10 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     fence_barrier_init();
     __syncwarp();
   }
+  if (warp == L::MMA_WARP) {
+    tmem_alloc(smem_u32(misc + 1), L::TMEM_COLS);
+    tmem_relinquish();
+  }
   griddep_wait();
   if (warp == L::REC_WARP) {
     int expert = 0, start = block * BT, count = BT;
@@ -223,13 +227,24 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     else
       expert = w4_find_block(p, block, BT, lane, &start, &count);
     if (lane == 0) {
-      misc[2] = expert, misc[3] = count, misc[4] = start;
+      misc[2] = expert, misc[3] = count;
       if (expert >= 0) load_records(expert, 0, early);
     }
     __syncwarp();
-  } else if (warp == L::MMA_WARP) {
-    tmem_alloc(smem_u32(misc + 1), L::TMEM_COLS);
-    tmem_relinquish();
+  } else if (warp >= L::X_WARP) {
+    // the block's rows (every warp finds the block for itself)
+    int start = block * BT, count = BT;
+    if (p.offsets == nullptr)
+      count = static_cast<int>(p.M - start < BT ? p.M - start : BT);
+    else if (w4_find_block(p, block, BT, lane, &start, &count) < 0)
+      count = 0;
+    for (int i = tid - L::X_WARP * 32; i < BT; i += L::X_THREADS) {
+      int32_t row = i >= count ? -1 : p.offsets ? p.order[start + i] : start + i;
+      if (row < 0 || row >= p.M) row = -1;
+      yrow[i] = row;
+      xrow[i] = row < 0 ? -1 : p.div == 1 ? row : row / p.div;
+    }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -346,7 +361,6 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     for (int i = max(0, issued - L::RS); i < issued; ++i)
       mbar_drain(r_full + 8 * (i % L::RS), (i / L::RS) & 1, budget);
   } else if (p.offsets == nullptr) {
-    for (int i = tid - L::X_WARP * 32; i < BT; i += L::X_THREADS) yrow[i] = i < count ? misc[4] + i : -1;
     // ---- token rows of one matrix: TMA; rows past M and k past K read as zero
     if (warp == L::X_WARP && lane == 0) {
       int issued = 0;
@@ -374,13 +388,6 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     // thread's arrival fires when its copies have landed, so the ring fills ahead
     constexpr int LANES = 8 * L::XB, ROWS = L::X_THREADS / LANES;
     const int lt = tid - L::X_WARP * 32;
-    for (int i = lt; i < BT; i += L::X_THREADS) {
-      int32_t row = i < count ? p.order[misc[4] + i] : -1;
-      if (row < 0 || row >= p.M) row = -1;
-      yrow[i] = row;
-      xrow[i] = row < 0 ? -1 : p.div == 1 ? row : row / p.div;
-    }
-    named_bar_sync(1, L::X_THREADS);
     const int c = lt & (LANES - 1), r0 = lt / LANES;
     const uint32_t at = static_cast<uint32_t>(c >> 3) * (BT * 128) + r0 * 128 + (((c & 7) ^ (r0 & 7)) << 4);
     const __half* src[BT / ROWS];  // rows r0 + ROWS j: row & 7 does not depend on j
@@ -411,7 +418,6 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     cp_async_wait_all();
   }
   __syncwarp();
-  __syncthreads();  // yrow
 
   // ---- epilogue
   mbar_wait_bounded(d_full, 0, budget > 100000000ull ? budget : 100000000ull);
