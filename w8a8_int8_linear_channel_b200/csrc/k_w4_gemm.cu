@@ -18,13 +18,13 @@
 // TMA producer, or four warps of cp.async where an expert's rows lie scattered.
 // All waits are bounded.
 //
-// 16384 x 4096 at 2048 tokens: 221 us, 1.24 PFLOP/s (0.74 of the measured matrix
-// product; tensor pipe 62% of active cycles).  What the rest is was measured by
-// leaving work out: 199 us without the arithmetic on the codes, 203 without
-// writing y, 182 with a quarter of the MMAs -- a K tile's chain of record,
-// operand, MMA and release, and about 5 us of start and finish per CTA, which
-// one CTA per SM cannot cover.  For few tokens the chain per K tile is all:
-// 4096 x 16384 at 16 tokens 19.4 us.
+// 16384 x 4096 at 2048 tokens: 212 us, 1.30 PFLOP/s (0.77 of the measured matrix
+// product).  A CTA of 32 K tiles takes 5700 cycles until its first
+// MMA (setup and tensor memory 2900, the record's latency 700, the first operand 1500),
+// 1230 per K tile (1024 for the MMAs at full rate; 1160 are left with 14 tokens: the
+// chain of record, operand, MMA and release) and some 5000 from the last MMA to its
+// end, which one CTA per SM cannot cover.  For few tokens the chain per K
+// tile is all: 4096 x 16384 at 16 tokens 18.4 us.
 //
 // Tensor memory never has to be waited for: a CTA takes 256 columns and its
 // shared memory lets two of them share an SM, or 512 and one.
@@ -78,13 +78,36 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Columns [col, col + 16) of the warp's lanes, complete on return.
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
-  tmem_ld_32x32b_x16(taddr, r);
+// Of registers that a load from tensor memory is writing.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
+               : "memory");
+}
+
+// Columns [col, col + 16) of the warp's lanes, complete on return.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
+  tmem_ld_32x32b_x16(taddr, r);
+  tmem_ld_wait(r);
+}
+
+// 16 lanes x 32 columns; register 4 i + j of thread t: lane t / 4 (+ 8 for j = 2, 3), column 8 i + 2 (t % 4) + (j & 1).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Four 8 x 8 matrices of fp16, as mma fragments hold them, stored transposed:
+// the lane's address is that of one row of eight.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
                : "memory");
 }
 
@@ -432,7 +455,43 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   const int es = p.y ? 2 : 4;
   const bool staged = slices == 1 && (p.w.N * es) % 16 == 0;
   const uint32_t pitch = RT * kW4Rows * es + 16;
-  if (warp < L::DEQ) {
+  if (staged && p.y && warp < L::DEQ) {
+    // fp16: fragments of 8 channels x 8 tokens, rounded and stored transposed
+    // (2048 x 16384 x 4096: 212 us, one value at a time 219)
+    const int t = RT == 2 ? (warp >> 2) & 1 : 0;
+    const int c0 = (warp >> (RT == 2 ? 3 : 2)) * (BT / 2), c1 = c0 + BT / 2;
+    const uint32_t d = tmem + t * BT + (static_cast<uint32_t>(warp & 3) << 21);
+    float bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t ch = static_cast<int64_t>(tile + t) * kW4Rows + (warp & 3) * 32 + (lane >> 2) + 8 * j;
+      bias[j] = p.bias && ch < p.w.N ? __half2float(p.bias[static_cast<int64_t>(expert) * p.w.N + ch]) : 0.0f;
+    }
+    // lane l's row: token l % 8 of the fragment, channels 8 (l / 8) ..
+    const uint32_t at = sbase + (lane & 7) * pitch + (t * kW4Rows + (warp & 3) * 32 + (lane >> 3) * 8) * 2;
+    for (int col = c0; col < c1; col += 32) {
+      if (col >= count) break;
+      __syncwarp();
+      uint32_t v[2][16];
+      tmem_ld_16x256b_x4(d + col, v[0]);
+      tmem_ld_16x256b_x4(d + col + (16u << 16), v[1]);
+      tmem_ld_wait(v[0]);
+      tmem_ld_wait(v[1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float lo = __uint_as_float(v[j >> 1][4 * i + 2 * (j & 1)]), hi = __uint_as_float(v[j >> 1][4 * i + 2 * (j & 1) + 1]);
+          if (p.bias) lo = __fadd_rn(lo, bias[j]), hi = __fadd_rn(hi, bias[j]);
+          if (p.relu) lo = lo > 0.0f ? lo : 0.0f, hi = hi > 0.0f ? hi : 0.0f;
+          const __half2 h = __floats2half2_rn(lo, hi);
+          m[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        stmatrix_x4_trans(at + (col + 8 * i) * pitch, m[0], m[1], m[2], m[3]);
+      }
+    }
+  } else if (warp < L::DEQ) {
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const int t = RT == 2 ? (warp >> 2) & 1 : 0;
@@ -463,11 +522,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
           if (p.bias) f = __fadd_rn(f, bias);
           if (p.relu) f = f > 0.0f ? f : 0.0f;
           if (staged) {
-            uint8_t* at = smem + (col + j) * pitch + (t * kW4Rows + r) * es;
-            if (p.y)
-              *reinterpret_cast<__half*>(at) = __float2half_rn(f);
-            else
-              *reinterpret_cast<float*>(at) = f;
+            *reinterpret_cast<float*>(smem + (col + j) * pitch + (t * kW4Rows + r) * 4) = f;
           } else {
             const int32_t row = yrow[col + j];
             if (row < 0 || ch >= p.w.N) continue;
