@@ -177,7 +177,7 @@ struct Layout {
 
 template <int BT, int RT, int G, bool ZERO>
 __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 : 2)
-    k_w4_gemm(const __grid_constant__ CUtensorMap tmX, const W4Product p, int slices, int blocks, int KT,
+    k_w4_gemm(const __grid_constant__ CUtensorMap tmX, const W4Product p, int nslices, int blocks, int KT,
               uint32_t* status, uint64_t budget) {
   using L = Layout<BT, RT, G, ZERO>;
   constexpr int NG = kW4K / G;
@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   int32_t* yrow = reinterpret_cast<int32_t*>(smem + L::YROW);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
+  const int slices = RT == 2 ? 1 : nslices;
   const int slice = blockIdx.x % slices;
   const int block = blockIdx.x / slices % blocks;
   const int tile = blockIdx.x / slices / blocks * RT;  // first weight tile
@@ -201,8 +202,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   const uint32_t r_full = done + 8 * L::XS, r_empty = r_full + 8 * L::RS;
   const uint32_t a_full = r_empty + 8 * L::RS, d_full = a_full + 8 * L::AS;
 
-  const int kt0 = static_cast<int>(static_cast<int64_t>(KT) * slice / slices);
-  const int n = static_cast<int>(static_cast<int64_t>(KT) * (slice + 1) / slices) - kt0;
+  const int kt0 = KT * slice / slices, n = KT * (slice + 1) / slices - kt0;  // this CTA's K tiles
   const int64_t nt = p.w.nt();
 
   // Until the first MMA a CTA waits for three latencies in a row (which expert,
