@@ -18,13 +18,13 @@
 // TMA producer, or four warps of cp.async where an expert's rows lie scattered.
 // All waits are bounded.
 //
-// 16384 x 4096 at 2048 tokens: 212 us, 1.30 PFLOP/s (0.77 of the measured matrix
-// product).  A CTA of 32 K tiles takes 5700 cycles until its first
-// MMA (setup and tensor memory 2900, the record's latency 700, the first operand 1500),
-// 1230 per K tile (1024 for the MMAs at full rate; 1160 are left with 14 tokens: the
-// chain of record, operand, MMA and release) and some 5000 from the last MMA to its
-// end, which one CTA per SM cannot cover.  For few tokens the chain per K
-// tile is all: 4096 x 16384 at 16 tokens 18.4 us.
+// 16384 x 4096 at 2048 tokens: 211 us, 1.30 PFLOP/s (0.77 of the measured matrix
+// product).  Of a CTA of 32 K tiles, about 49,000 cycles, some 4500 pass until its
+// first MMA (which block, tensor memory, a record's latency, the first
+// operand), 1240 per K tile (1024 for the MMAs at full rate; 1160 are left with 14
+// tokens: the chain of record, operand, MMA and release) and 4700 from the last MMA to
+// its end; with one CTA per SM nothing covers the two ends.  For few tokens
+// the chain per K tile is all: 4096 x 16384 at 16 tokens 18.4 us.
 //
 // Tensor memory never has to be waited for: a CTA takes 256 columns and its
 // shared memory lets two of them share an SM, or 512 and one.
@@ -209,22 +209,13 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   // its records, the operand made of them); what can go beside them does:
   // one warp sets up the barriers, finds the block and sends for its first
   // records, while another takes tensor memory and the last ones look up the rows.
-  // (records of K tiles [from, to); returns how many were sent for)
-  auto load_records = [&](int expert, int from, int to) {
-    for (int i = from; i < to; ++i) {
-      const uint32_t rs = i % L::RS;
-      if (!w4_wait(r_empty + 8 * rs, i / L::RS & 1 ^ 1, budget, status, abort)) return i;
-      // the last weight tile may stand alone: its place is taken by itself
-      // again, and nothing of the copy is written out
-      mbar_arrive_expect_tx(r_full + 8 * rs, RT * L::REC);
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const int64_t wt = tile + t < nt ? tile + t : nt - 1;
-        bulk_load(sbase + L::R + (rs * RT + t) * L::REC,
-                  p.w.data + ((static_cast<int64_t>(expert) * nt + wt) * KT + kt0 + i) * L::REC, L::REC, r_full + 8 * rs);
-      }
-    }
-    return to;
+  // (the record of weight tile t and K tile i, to be counted on its stage's barrier)
+  auto load_record = [&](int expert, int i, uint32_t rs, int t) {
+    // the last weight tile may stand alone: its place is taken by itself
+    // again, and nothing of the copy is written out
+    const int64_t wt = tile + t < nt ? tile + t : nt - 1;
+    bulk_load(sbase + L::R + (rs * RT + t) * L::REC,
+              p.w.data + ((static_cast<int64_t>(expert) * nt + wt) * KT + kt0 + i) * L::REC, L::REC, r_full + 8 * rs);
   };
   const int early = n < L::RS ? n : L::RS;
   if (warp == L::REC_WARP) {
@@ -249,10 +240,10 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       count = static_cast<int>(p.M - start < BT ? p.M - start : BT);
     else
       expert = w4_find_block(p, block, BT, lane, &start, &count);
-    if (lane == 0) {
-      misc[2] = expert, misc[3] = count;
-      if (expert >= 0) load_records(expert, 0, early);
-    }
+    if (lane == 0) misc[2] = expert, misc[3] = count;
+    if (lane < early && expert >= 0) mbar_arrive_expect_tx(r_full + 8 * lane, RT * L::REC);
+    __syncwarp();
+    if (lane < early * RT && expert >= 0) load_record(expert, lane / RT, lane / RT, lane % RT);
     __syncwarp();
   } else if (warp >= L::X_WARP) {
     // the block's rows (every warp finds the block for itself)
@@ -379,7 +370,15 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     if (leader) mma_commit(d_full);  // also after a wait that ran out: nothing in flight is left behind
   } else if (warp == L::REC_WARP) {
     // ---- record producer
-    const int issued = lane == 0 ? load_records(expert, early, n) : 0;
+    int issued = lane == 0 ? early : 0;  // (the other lanes wait for nothing)
+    for (int i = early; i < n && lane == 0; ++i) {
+      const uint32_t rs = i % L::RS;
+      if (!w4_wait(r_empty + 8 * rs, (i / L::RS & 1) ^ 1, budget, status, abort)) break;
+      mbar_arrive_expect_tx(r_full + 8 * rs, RT * L::REC);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) load_record(expert, i, rs, t);
+      issued = i + 1;
+    }
     // records in flight land before the CTA can leave (at once unless a wait ran out)
     for (int i = max(0, issued - L::RS); i < issued; ++i)
       mbar_drain(r_full + 8 * (i % L::RS), (i / L::RS) & 1, budget);
