@@ -582,9 +582,9 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
 // Slices of K per weight tile (the cluster size).  A CTA's time is taken as
 // 0.39 us per K tile (0.59 with 128 tokens), 4.5 for start and finish and 4
 // more for the cluster's sum (4096 x 4096 at 64 tokens: 17.0 us with one slice,
-// 11.5 with four).  Two CTAs on an
+// 11.5 with four, 10.7 by now).  Two CTAs on an
 // SM overlap their tiles, hardly the rest: with clusters until every SM has
-// two, 4096 x 4096 at 384 tokens took 41.1 us, with one slice 26.4.  Clusters
+// two, 4096 x 4096 at 384 tokens took 41.1 us, with one slice 26.4 (19.8 by now).  Clusters
 // of more than two do not pack every SM of a GPC; an eighth is taken off
 // (4096 x 16384 at 384 tokens: 288 CTAs in threes 86.7 us, in twos 70.3).
 int pick_slices(int64_t units, int64_t kt, int bt, int num_sms) {
@@ -646,18 +646,18 @@ cudaError_t launch_g(const W4Product& p, const Ctx& c) {
 
 cudaError_t launch_w4_gemm(const W4Product& p, const Ctx& c, int64_t tokens) {
   // Blocks of 64 tokens or 128.  A block's MMAs are only as wide as it has
-  // tokens, so narrower blocks would save nothing (16384 x 4096 at 16 tokens
-  // takes 17.2 us with blocks of 16, 32 or 64).  An expert's tokens scatter around the average, and a
-  // second block makes its weight's operand once more: 64 experts with 12
-  // tokens each, blocks of 16 / 32 / 64 / 128: 273 / 239 / 225 / 231 us a layer, with 20:
-  // 376 / 262 / 243 / 239, with 32: 500 / 329 / 270 / 252.
+  // tokens, so narrower blocks would save nothing (16384 x 4096 at 16 tokens took
+  // the same with blocks of 16, 32 or 64).  An expert's tokens scatter around the
+  // average, and a second block makes its weight's operand once more: 64 experts
+  // with 12 tokens each, blocks of 64 / 128: 217 / 219 us a layer, with 20 230 /
+  // 227, with 32 249 / 236 (blocks of 16 with 12 tokens a fifth more than of 64).
   if (tokens <= (p.offsets ? 16 : 64)) return launch_g<64, 1>(p, c);
   // One weight tile per CTA and two CTAs per SM, or two tiles and one CTA, which
-  // halves the token traffic: 2.05 against 1.94 us per 128 x 256 x 4096 and SM
-  // (16384 x 4096 at 2048 tokens 233 and 220 us), for experts, whose rows come
-  // without TMA, 540 and 458 us a layer of 1024 tokens.  But 384 tokens, 192
-  // large CTAs, take 64.2 us and 384 small ones 51.8; and where large CTAs would
-  // not cover the SMs only small ones can be sliced along K.
+  // halves the token traffic: 16384 x 4096 at 2048 tokens 223 and 213 us (a large
+  // CTA 0.95 of two small ones), for experts, whose rows come without TMA,
+  // 506 and 419 us a layer of 1024 tokens.  But 384 tokens, 192 large CTAs, take 57.3
+  // us and 384 small ones 47.8; and where large CTAs would not cover the SMs only
+  // small ones can be sliced along K.
   const int64_t blocks = w4_blocks(p, 128), nt = p.w.nt();
   const int64_t pairs = blocks * ((nt + 1) / 2);
   const int64_t small = (blocks * nt + c.num_sms - 1) / c.num_sms, large = (pairs + c.num_sms - 1) / c.num_sms;

@@ -384,12 +384,12 @@ int64_t w4_blocks(const W4Product& p, int bt) {
 // Which kernel.  Up to eight tokens per weight tile always this one.  With
 // more it reads the weight once per eight tokens, which still pays where an SM
 // has little to do altogether (starting the tensor cores' pipeline takes 3 us
-// longer): 1024 x 1024 at 64 tokens 3.4 us here, 9.9 there; 4096 x 4096 at 16
-// tokens 7.1 and 9.1, at 24 10.2 and 9.5; 4096 x 16384 at 16 29.4 and 19.8.
+// longer): 1024 x 1024 at 64 tokens 3.5 us here, 9.9 there; 4096 x 4096 at 16
+// tokens 7.0 and 9.1, at 24 10.2 and 9.0; 4096 x 16384 at 16 29.4 and 18.4.
 // Experts' tokens scatter around the average (most of them still need one
-// block of eight): 64 experts with 10 tokens each 210 us a layer here and 222
-// there, with 12 242 and 225; 256 small experts with 10 122 and 129, with 16
-// 162 and 136.
+// block of eight): 64 experts with 10 tokens each 207 us a layer here and 222
+// there, with 12 242 and 217; 256 small experts with 10 122 and 129, with 16
+// 162 and 130.
 constexpr int kTilesPerSm = 32;    // 64 channels x 128 k x eight tokens
 constexpr int kTokensExperts = 10;
 
