@@ -384,3 +384,30 @@ def test_wait_that_runs_out_is_reported(cuda_device, M):
         sq.sq_set_wait_budget_ns(2_000_000_000)
     y = sq.sq_w4a16_linear(x, w4, torch.empty_like(good))
     assert sq.sq_poll_status() == 0 and torch.equal(y, good)
+
+
+@pytest.mark.gpu
+def test_products_beside_the_int8_linear(cuda_device):
+    """4-bit and INT8 linears on two streams at once, whose CTAs share SMs and tensor memory: the bits
+    of each running alone."""
+    import w8a8_int8_linear_channel_b200 as sq
+    rng = np.random.default_rng(12)
+    N, K = 2048, 2064
+    w = dev((rng.standard_normal((N, K)) * 0.05).astype(np.float16))
+    calib = dev(_tokens(rng, 64, K))
+    int8, w4 = sq.SmoothQuantLinear.from_float(w, calib), sq.W4Linear.from_float(w)
+    xs = [dev(_tokens(rng, M, K)) for M in (1, 40, 100, 500, 1200)]
+    alone = [(int8(x).clone(), w4(x).clone()) for x in xs]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        a, b = [], []
+        for x in xs:
+            with torch.cuda.stream(s1):
+                a.append(w4(x))
+            with torch.cuda.stream(s2):
+                b.append(int8(x).clone())
+        torch.cuda.synchronize()
+        assert sq.sq_poll_status() == 0
+        for (y8, y4), p, q in zip(alone, a, b):
+            assert torch.equal(y4, p) and torch.equal(y8, q)

@@ -580,13 +580,13 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
 }
 
 // Slices of K per weight tile (the cluster size).  A CTA's time is taken as
-// 0.39 us per K tile (0.59 with 128 tokens), 4.5 for start and finish and 4
-// more for the cluster's sum (4096 x 4096 at 64 tokens: 17.0 us with one slice,
-// 11.5 with four, 10.7 by now).  Two CTAs on an
-// SM overlap their tiles, hardly the rest: with clusters until every SM has
-// two, 4096 x 4096 at 384 tokens took 41.1 us, with one slice 26.4 (19.8 by now).  Clusters
-// of more than two do not pack every SM of a GPC; an eighth is taken off
-// (4096 x 16384 at 384 tokens: 288 CTAs in threes 86.7 us, in twos 70.3).
+// 0.39 us per K tile (0.59 with 128 tokens), 4.5 for start and finish and 4 more
+// for the cluster's sum (4096 x 4096 at 64 tokens: 17.0 us with one slice, 11.5
+// with four, 10.7 by now).  Two CTAs on an SM overlap their tiles, hardly the
+// rest: with clusters until every SM has two, 4096 x 4096 at 384 tokens took
+// 41.1 us, with one slice 26.4 (19.8 by now).  Clusters of more than two do not
+// pack every SM of a GPC; an eighth is taken off (4096 x 16384 at 384 tokens:
+// 288 CTAs in threes 86.7 us, in twos 70.3).
 int pick_slices(int64_t units, int64_t kt, int bt, int num_sms) {
   int slices = 1;
   int64_t best = INT64_MAX;
