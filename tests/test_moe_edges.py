@@ -1,0 +1,27 @@
+"""Expert routing and the pair plan where a shortcut could differ from the definition."""
+import numpy as np
+import pytest
+
+from test_moe import _check_route, _route
+
+
+@pytest.mark.gpu
+def test_route_group_scores_that_cancel(cuda_device):
+    # 1000 + p and p - 1000: the scores 1.2822052 and 1.2821990 differ by less than the rounding of
+    # their parts in 32 bits
+    l = np.array([[-0.37785533, 1.9510481, 0.55182946, 0.60867757]], np.float32)
+    bias = np.array([1000, -1000, 1000, -1000], np.float32)
+    ids, _ = _route(l, 1, bias, score="sigmoid", n_group=2, topk_group=1, group_top=2)
+    assert ids.tolist() == [[0]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n_group,topk_group,topk", [(4, 2, 1, 1), (8, 2, 1, 3), (32, 4, 2, 6), (256, 8, 4, 8)])
+@pytest.mark.parametrize("size", [30.0, 1000.0, 1e5])
+def test_route_groups_under_a_large_bias_of_either_sign(cuda_device, E, n_group, topk_group, topk, score, size):
+    # the first of every group's experts far up, the others far down: a group's score is what is left
+    rng = np.random.default_rng(int(E + size))
+    l = (rng.standard_normal((3000, E)) * 1.5).astype(np.float32)
+    bias = np.where(np.arange(E) % (E // n_group) == 0, size, -size).astype(np.float32)
+    _check_route(l, topk, bias, score=score, n_group=n_group, topk_group=topk_group, group_top=2)

@@ -209,8 +209,10 @@ __device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, int l
 // 2^-12 are at least 2^-36 apart, which a score shows.  With them, a 32-bit choice is within
 // 2^-18 + 2^-19 |c| of the exact one: the exponential is off by 2^-20 relatively
 // (its argument up to 2^-19 where the score is then next to 0 or 1), a sum of up to 512 exponentials by
-// 2^-19, and score and choice are rounded.  Two choices (a group's score is one or two of them)
-// whose 32-bit values differ by more than four times that are in their exact order.  With
+// 2^-19, and score and choice are rounded.  Two choices whose 32-bit values differ by
+// more than four times that are in their exact order.  So are two groups' scores, but a score of
+// two choices c + d is only within 2^-17 + 2^-18 (|c| + |d|): a bias may give them
+// opposite signs, so their magnitudes count, not the sum's.  With
 // 256 experts under a bias about one token in fifty is not sure.
 template <int V>
 __device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, int lane) {
@@ -251,8 +253,11 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, int la
 #pragma unroll
     for (int v = 0; v < V; ++v) c[v] = l[v];
   }
-  auto apart = [](float larger, float smaller) {
-    return __fadd_rn(larger, -smaller) > 0x1p-16f + 0x1p-17f * fmaxf(fabsf(larger), fabsf(smaller));
+  auto apart_by = [](float larger, float smaller, float magnitude) {
+    return __fadd_rn(larger, -smaller) > 0x1p-16f + 0x1p-17f * magnitude;
+  };
+  auto apart = [&](float larger, float smaller) {
+    return apart_by(larger, smaller, fmaxf(fabsf(larger), fabsf(smaller)));
   };
 
   if (groups) {
@@ -267,8 +272,13 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, int la
       second = fmaxf(fmaxf(second, s2), fminf(first, f));
       first = fmaxf(first, f);
     }
-    float score = a.group_top == 2 && second > -INFINITY ? __fadd_rn(first, second) : first;
+    const bool two = a.group_top == 2 && second > -INFINITY;
+    float score = two ? __fadd_rn(first, second) : first;
     if (lane * V >= E) score = -INFINITY;
+    // the largest magnitude that any group's score is made of (its bits are in its order)
+    const float parts = two ? __fadd_rn(fabsf(first), fabsf(second)) : fabsf(first);
+    const float magnitude =
+        __uint_as_float(__reduce_max_sync(kAll, score == -INFINITY ? 0u : __float_as_uint(parts)));
     bool keep = false;
     float before = INFINITY;
     for (int j = 0; j <= a.topk_group; ++j) {
@@ -276,7 +286,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, int64_t t, int la
       const float value = order_value(best);
       if (best == kNegInfKey) break;
       if (j == a.topk_group) {
-        if (!apart(before, value)) return false;  // the last group kept and the first one left out
+        if (!apart_by(before, value, magnitude)) return false;  // the last group kept and the first one left out
         break;
       }
       before = value;
