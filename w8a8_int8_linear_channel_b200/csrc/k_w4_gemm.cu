@@ -132,6 +132,10 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, f
                : "memory");
 }
 
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // BT tokens and RT weight tiles (128 channels each) per CTA.
 template <int BT, int RT, int G, bool ZERO>
 struct Layout {
@@ -442,11 +446,21 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   __syncwarp();
 
   // ---- epilogue
-  mbar_wait_bounded(d_full, 0, budget > 100000000ull ? budget : 100000000ull);
+  // The warps that read the sums wait for the last MMAs.  If that wait or one before
+  // it ran out, the status word says so and this CTA stores nothing; the MMAs that
+  // were issued are waited for all the same, since they still read shared memory.
+  if (warp < L::DEQ && !w4_wait_warp(d_full, 0, budget, status, abort)) mbar_drain(d_full, 0, budget);
   __syncwarp();
+  tc_fence_before();
+  __syncthreads();
   tc_fence_after();
+  const bool ok = *abort == 0;  // the same in every warp: no wait follows
   griddep_launch_dependents();
-  if (slices > 1) cluster_sync_all();  // the token stages of every CTA are free
+  if (slices > 1) {
+    cluster_sync_all();  // the token stages of every CTA are free
+    // the cluster's sum needs every slice
+    if (!ok && tid < slices) st_cluster_u32(mapa_shared(smem_u32(misc), tid), 1);
+  }
   // Without slices a tile goes out through shared memory (every stage is free
   // by now), so that a warp writes 512 consecutive bytes of a row; written
   // from the accumulators' own layout, 32 channels of one token per store, a
@@ -454,7 +468,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
   const int es = p.y ? 2 : 4;
   const bool staged = slices == 1 && (p.w.N * es) % 16 == 0;
   const uint32_t pitch = RT * kW4Rows * es + 16;
-  if (staged && p.y && warp < L::DEQ) {
+  if (ok && staged && p.y && warp < L::DEQ) {
     // fp16: fragments of 8 channels x 8 tokens, rounded and stored transposed
     // (2048 x 16384 x 4096: 212 us, one value at a time 219)
     const int t = RT == 2 ? (warp >> 2) & 1 : 0;
@@ -490,7 +504,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
         stmatrix_x4_trans(at + (col + 8 * i) * pitch, m[0], m[1], m[2], m[3]);
       }
     }
-  } else if (warp < L::DEQ) {
+  } else if (ok && warp < L::DEQ) {
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const int t = RT == 2 ? (warp >> 2) & 1 : 0;
@@ -535,7 +549,7 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
       }
     }
   }
-  if (staged) {
+  if (ok && staged) {
     __syncthreads();
     // 16-byte pieces; a row's pieces go to consecutive lanes
     const int per = RT * kW4Rows * es / 16;  // a power of two
@@ -557,7 +571,8 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
     const int64_t n0 = static_cast<int64_t>(tile) * kW4Rows + slice * share;
     const int64_t left = min(p.w.N - n0, static_cast<int64_t>(kW4Rows - slice * share));
     const int width = static_cast<int>(left < share ? left : share);
-    for (int i = tid; i < width * count; i += L::THREADS) {
+    const int todo = *abort == 0 ? width * count : 0;
+    for (int i = tid; i < todo; i += L::THREADS) {
       const int tk = i / width, q = i - tk * width;
       const int32_t row = yrow[tk];
       if (row < 0) continue;
