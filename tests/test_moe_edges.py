@@ -1,6 +1,10 @@
 """Expert routing and the pair plan where a shortcut could differ from the definition."""
 import numpy as np
 import pytest
+import torch
+
+import w4_ref as ref
+from gpu_util import dev, host
 
 from test_moe import _check_route, _route
 
@@ -25,3 +29,26 @@ def test_route_groups_under_a_large_bias_of_either_sign(cuda_device, E, n_group,
     l = (rng.standard_normal((3000, E)) * 1.5).astype(np.float32)
     bias = np.where(np.arange(E) % (E // n_group) == 0, size, -size).astype(np.float32)
     _check_route(l, topk, bias, score=score, n_group=n_group, topk_group=topk_group, group_top=2)
+
+
+def test_plan_workspace_does_not_grow_with_the_pairs():
+    # every CTA reads the whole workspace, so with a chunk per 2048 pairs the work grew with their square
+    import w8a8_int8_linear_channel_b200 as sq
+    assert sq.sq_moe_plan_workspace_bytes(2**31 - 1, 512) <= 512 * 512 * 4
+    assert sq.sq_moe_plan_workspace_bytes(65536, 256) == 32 * 256 * 4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pairs,E", [(2048 * 512, 64), (2048 * 512 + 1, 3), (2048 * 1024 + 1, 512), (5_000_001, 40),
+                                     (8_388_611, 257)])
+def test_plan_many_pairs(cuda_device, pairs, E):
+    import w8a8_int8_linear_channel_b200 as sq
+    rng = np.random.default_rng(pairs)
+    skewed = np.minimum(rng.geometric(0.3, pairs) - 1, E)  # some past the experts
+    for ids in (rng.integers(-1, E, pairs), skewed, np.full(pairs, -1), np.full(pairs, E - 1)):
+        ids = ids.astype(np.int32)
+        off = torch.full((E + 1,), -7, dtype=torch.int32, device="cuda")
+        order = torch.full((pairs,), -7, dtype=torch.int32, device="cuda")
+        sq.sq_moe_plan(dev(ids), off, order)
+        r_off, r_order = ref.plan(ids, E)
+        assert np.array_equal(host(off), r_off) and np.array_equal(host(order), r_order)

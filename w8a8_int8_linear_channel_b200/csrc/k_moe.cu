@@ -397,115 +397,138 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_moe_route(const RouteArgs 
 // ------------------------------------------------------------------ plan ----
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanChunk = 2048;  // pairs per CTA
-constexpr int kPerWarp = kPlanChunk / kPlanWarps;
+constexpr int kPlanPart = 2048;  // pairs sorted at a time
+constexpr int kPerWarp = kPlanPart / kPlanWarps;
+constexpr int kPlanChunks = 512;  // CTAs at most
+
+// Parts per CTA, and CTAs.
+struct PlanShape {
+  int parts, chunks;
+};
+PlanShape plan_shape(int64_t P) {
+  const int64_t all = (P + kPlanPart - 1) / kPlanPart;
+  const int64_t parts = (all + kPlanChunks - 1) / kPlanChunks;
+  return {static_cast<int>(parts), static_cast<int>((all + parts - 1) / parts)};
+}
 
 __global__ void __launch_bounds__(kPlanThreads)
-    k_plan_count(const int32_t* __restrict__ ids, int64_t P, int E, int32_t* __restrict__ counts) {
+    k_plan_count(const int32_t* __restrict__ ids, int64_t P, int E, int64_t chunk, int32_t* __restrict__ counts) {
   extern __shared__ int32_t hist[];
   griddep_wait();
   griddep_launch_dependents();
   for (int e = threadIdx.x; e < E; e += kPlanThreads) hist[e] = 0;
   __syncthreads();
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * kPlanChunk;
-  for (int i = threadIdx.x; i < kPlanChunk && base + i < P; i += kPlanThreads) {
-    const int e = ids[base + i];
+  const int64_t end = min(P, (blockIdx.x + 1) * chunk);
+  for (int64_t q = blockIdx.x * chunk + threadIdx.x; q < end; q += kPlanThreads) {
+    const int e = ids[q];
     if (e >= 0 && e < E) atomicAdd(&hist[e], 1);  // integer counts: any order gives the same
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kPlanThreads) counts[static_cast<int64_t>(blockIdx.x) * E + e] = hist[e];
 }
 
-// Chunks of 2048 pairs: up to that many one CTA does it all, in 2.4 us; 65536 pairs
-// of 256 experts take 10 us in two launches, both latency (each CTA adds up
-// the histograms of all chunks itself instead of a third launch).
+// A stable counting sort, 2048 pairs (a part) at a time: counts per warp and
+// expert, their scan, then every warp places its pairs in their order.
 //
-// A stable counting sort of one chunk: counts per warp and expert, a scan
-// over experts, then every warp places its pairs in their order.  With more
-// than one chunk `counts` holds every chunk's histogram.
+// Up to 2048 pairs one CTA does it all (64 pairs in 3.1 us, 2048 in 5.7).  More are
+// split into chunks of one or more parts, whose histograms `counts` holds: every CTA
+// adds up all of them itself instead of a third launch (65536 pairs of 256 experts take 9.8 us in
+// two launches, both latency).  That work grows with the square of the number of chunks, so
+// there are 512 at most and a CTA takes its parts one after the other: 2^20 / 2^22 / 2^24 pairs
+// take 58 / 88 / 253 us, with at most 256 chunks 44 / 104 / 373, with 1024 54 / 189 / 351, and 2^22
+// with a chunk per part 370.
 __global__ void __launch_bounds__(kPlanThreads)
     k_plan_place(const int32_t* __restrict__ ids, int64_t P, int E, const int32_t* __restrict__ counts, int chunks,
-                 int32_t* __restrict__ offsets, int32_t* __restrict__ order) {
+                 int parts, int32_t* __restrict__ offsets, int32_t* __restrict__ order) {
   extern __shared__ int32_t sh32[];
   int32_t* wcount = sh32;                  // [warps][E]
   int32_t* total = sh32 + kPlanWarps * E;  // [E + 1]: pairs of all chunks, then their exclusive scan
-  int32_t* base = total + E + 1;           // [E]: pairs of the chunks before this one
+  int32_t* base = total + E + 1;           // [E]: pairs of the chunks before this one, then where the next part's go
   __shared__ int32_t carry[kPlanWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
   griddep_launch_dependents();
-  for (int i = tid; i < kPlanWarps * E; i += kPlanThreads) wcount[i] = 0;
-  __syncthreads();
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanChunk + warp * kPerWarp;
-  int32_t mine[kPerWarp / 32];
+  for (int part = 0; part < parts; ++part) {
+    const int64_t start = (static_cast<int64_t>(blockIdx.x) * parts + part) * kPlanPart;
+    if (start >= P) break;
+    for (int i = tid; i < kPlanWarps * E; i += kPlanThreads) wcount[i] = 0;
+    __syncthreads();
+    const int64_t first = start + warp * kPerWarp;
+    int32_t mine[kPerWarp / 32];
 #pragma unroll
-  for (int i = 0; i < kPerWarp / 32; ++i) {
-    const int64_t q = first + 32 * i + lane;
-    mine[i] = q < P ? ids[q] : -1;
-    if (mine[i] >= E) mine[i] = -1;
-    if (mine[i] >= 0) atomicAdd(&wcount[warp * E + mine[i]], 1);
-  }
-  __syncthreads();
-  for (int e = tid; e < E; e += kPlanThreads) {
-    int32_t here = 0;
-    for (int w = 0; w < kPlanWarps; ++w) {
-      const int32_t n = wcount[w * E + e];
-      wcount[w * E + e] = here;  // pairs of this chunk's earlier warps
-      here += n;
+    for (int i = 0; i < kPerWarp / 32; ++i) {
+      const int64_t q = first + 32 * i + lane;
+      mine[i] = q < P ? ids[q] : -1;
+      if (mine[i] >= E) mine[i] = -1;
+      if (mine[i] >= 0) atomicAdd(&wcount[warp * E + mine[i]], 1);
     }
-    int32_t before = 0, all = here;
-    if (chunks > 1) {
-      all = 0;
+    __syncthreads();
+    if (part == 0) {
+      for (int e = tid; e < E; e += kPlanThreads) {
+        int32_t before = 0, all = 0;
+        if (chunks == 1) {
+          for (int w = 0; w < kPlanWarps; ++w) all += wcount[w * E + e];
+        } else {
 #pragma unroll 8
-      for (int c = 0; c < chunks; ++c) {
-        const int32_t n = counts[static_cast<int64_t>(c) * E + e];
-        if (c < static_cast<int>(blockIdx.x)) before += n;
-        all += n;
+          for (int c = 0; c < chunks; ++c) {
+            const int32_t n = counts[static_cast<int64_t>(c) * E + e];
+            if (c < static_cast<int>(blockIdx.x)) before += n;
+            all += n;
+          }
+        }
+        total[e] = all;
+        base[e] = before;
       }
-    }
-    total[e] = all;
-    base[e] = before;
-  }
-  __syncthreads();
-  // exclusive scan of total[0 .. E) in place, E <= 2 * kPlanThreads
-  int32_t a0 = 2 * tid < E ? total[2 * tid] : 0, a1 = 2 * tid + 1 < E ? total[2 * tid + 1] : 0;
-  int32_t inc = a0 + a1;
+      __syncthreads();
+      // exclusive scan of total[0 .. E) in place, E <= 2 * kPlanThreads
+      int32_t a0 = 2 * tid < E ? total[2 * tid] : 0, a1 = 2 * tid + 1 < E ? total[2 * tid + 1] : 0;
+      int32_t inc = a0 + a1;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t up = __shfl_up_sync(kAll, inc, o);
-    if (lane >= o) inc += up;
-  }
-  if (lane == 31) carry[warp] = inc;
-  __syncthreads();
-  int32_t pre = 0;
-  for (int w = 0; w < warp; ++w) pre += carry[w];
-  const int32_t ex = pre + inc - a0 - a1;
-  if (2 * tid < E) total[2 * tid] = ex;
-  if (2 * tid + 1 < E) total[2 * tid + 1] = ex + a0;
-  if (tid == kPlanThreads - 1) total[E] = pre + inc;
-  __syncthreads();
-  if (blockIdx.x == 0)
-    for (int e = tid; e <= E; e += kPlanThreads) offsets[e] = total[e];
-  for (int e = tid; e < E; e += kPlanThreads)
-    for (int w = 0; w < kPlanWarps; ++w) wcount[w * E + e] += total[e] + base[e];
-  // entries past the last routed pair
-  for (int64_t q = static_cast<int64_t>(blockIdx.x) * kPlanChunk + tid; q < P && q < static_cast<int64_t>(blockIdx.x + 1) * kPlanChunk;
-       q += kPlanThreads)
-    if (q >= total[E]) order[q] = -1;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kPerWarp / 32; ++i) {
-    const int e = mine[i];
-    const unsigned same = __match_any_sync(kAll, e);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    int32_t at = 0;
-    if (e >= 0) at = wcount[warp * E + e];
-    __syncwarp();
-    if (e >= 0) {
-      if (rank == 0) wcount[warp * E + e] = at + __popc(same);
-      order[at + rank] = static_cast<int32_t>(first + 32 * i + lane);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t up = __shfl_up_sync(kAll, inc, o);
+        if (lane >= o) inc += up;
+      }
+      if (lane == 31) carry[warp] = inc;
+      __syncthreads();
+      int32_t pre = 0;
+      for (int w = 0; w < warp; ++w) pre += carry[w];
+      const int32_t ex = pre + inc - a0 - a1;
+      if (2 * tid < E) total[2 * tid] = ex;
+      if (2 * tid + 1 < E) total[2 * tid + 1] = ex + a0;
+      if (tid == kPlanThreads - 1) total[E] = pre + inc;
+      __syncthreads();
+      if (blockIdx.x == 0)
+        for (int e = tid; e <= E; e += kPlanThreads) offsets[e] = total[e];
     }
-    __syncwarp();
+    // where each warp's pairs go, and where the next part's begin
+    for (int e = tid; e < E; e += kPlanThreads) {
+      int32_t at = base[e] + (part == 0 ? total[e] : 0);
+      for (int w = 0; w < kPlanWarps; ++w) {
+        const int32_t n = wcount[w * E + e];
+        wcount[w * E + e] = at;
+        at += n;
+      }
+      base[e] = at;
+    }
+    // entries past the last routed pair
+    for (int64_t q = start + tid; q < P && q < start + kPlanPart; q += kPlanThreads)
+      if (q >= total[E]) order[q] = -1;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPerWarp / 32; ++i) {
+      const int e = mine[i];
+      const unsigned same = __match_any_sync(kAll, e);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      int32_t at = 0;
+      if (e >= 0) at = wcount[warp * E + e];
+      __syncwarp();
+      if (e >= 0) {
+        if (rank == 0) wcount[warp * E + e] = at + __popc(same);
+        order[at + rank] = static_cast<int32_t>(first + 32 * i + lane);
+      }
+      __syncwarp();
+    }
+    __syncthreads();
   }
 }
 
@@ -580,20 +603,20 @@ cudaError_t launch_moe_route(const RouteArgs& a, const Ctx& c) {
 }
 
 size_t moe_plan_workspace_bytes(int64_t P, int E) {
-  const int64_t chunks = (P + kPlanChunk - 1) / kPlanChunk;
+  const int chunks = plan_shape(P).chunks;
   return chunks > 1 ? static_cast<size_t>(chunks) * E * sizeof(int32_t) : 0;
 }
 
 cudaError_t launch_moe_plan(const int32_t* ids, int64_t P, int E, int32_t* offsets, int32_t* order, int32_t* ws,
                             const Ctx& c) {
-  const int chunks = static_cast<int>((P + kPlanChunk - 1) / kPlanChunk);
-  if (chunks > 1) {
-    const cudaError_t e = launch_pdl(k_plan_count, dim3(chunks), dim3(kPlanThreads), sizeof(int32_t) * E, c.stream,
-                                     ids, P, E, ws);
+  const PlanShape s = plan_shape(P);
+  if (s.chunks > 1) {
+    const cudaError_t e = launch_pdl(k_plan_count, dim3(s.chunks), dim3(kPlanThreads), sizeof(int32_t) * E, c.stream,
+                                     ids, P, E, static_cast<int64_t>(s.parts) * kPlanPart, ws);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(k_plan_place, dim3(chunks), dim3(kPlanThreads), sizeof(int32_t) * ((kPlanWarps + 2) * E + 1),
-                    c.stream, ids, P, E, static_cast<const int32_t*>(ws), chunks, offsets, order);
+  return launch_pdl(k_plan_place, dim3(s.chunks), dim3(kPlanThreads), sizeof(int32_t) * ((kPlanWarps + 2) * E + 1),
+                    c.stream, ids, P, E, static_cast<const int32_t*>(ws), s.chunks, s.parts, offsets, order);
 }
 
 cudaError_t launch_moe_combine(const __half* y16, const float* y32, const int32_t* ids, const float* weights,
