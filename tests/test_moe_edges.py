@@ -52,3 +52,13 @@ def test_plan_many_pairs(cuda_device, pairs, E):
         sq.sq_moe_plan(dev(ids), off, order)
         r_off, r_order = ref.plan(ids, E)
         assert np.array_equal(host(off), r_off) and np.array_equal(host(order), r_order)
+
+
+def test_plan_refuses_a_workspace_whose_bytes_are_not_its_own():
+    # an expanded tensor counts 4 MB and owns one byte
+    import w8a8_int8_linear_channel_b200 as sq
+    ids, off = torch.zeros(100000, dtype=torch.int32), torch.zeros(65, dtype=torch.int32)
+    byte = torch.zeros(1, dtype=torch.uint8)
+    for ws in (byte.expand(1 << 22), torch.zeros(1 << 23, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            sq.sq_moe_plan(ids, off, torch.empty_like(ids), workspace=ws)

@@ -222,6 +222,8 @@ def sq_moe_plan(ids: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor, w
         _vec(offsets, E + 1, _I32, "offsets")
     if order.dtype != _I32 or order.numel() != pairs or not order.is_contiguous():
         _vec(order, pairs, _I32, "order")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: need a contiguous tensor")
     if workspace is None:
         need = int(_L.sq_moe_plan_workspace_bytes(pairs, E))
         if need:
