@@ -62,3 +62,40 @@ def test_plan_refuses_a_workspace_whose_bytes_are_not_its_own():
     for ws in (byte.expand(1 << 22), torch.zeros(1 << 23, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError, match="workspace"):
             sq.sq_moe_plan(ids, off, torch.empty_like(ids), workspace=ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,E", [(np.float16, 60), (np.float16, 13), (np.float32, 6)])
+def test_route_a_slice_of_rows(cuda_device, dtype, E):
+    # rows of 120 bytes and the like: a slice of a batch starts off 16 bytes
+    import w8a8_int8_linear_channel_b200 as sq
+    rng = np.random.default_rng(E)
+    T, topk = 9, 4
+    l = rng.standard_normal((T, E)).astype(dtype)
+    bias = dev((rng.standard_normal(E) * 0.1).astype(np.float32))
+    full = dev(l)
+    layer = sq.W4Experts.from_float(dev((rng.standard_normal((E, 64, 32)) * 0.1).astype(np.float16)),
+                                    dev((rng.standard_normal((E, 32, 64)) * 0.1).astype(np.float16)), topk,
+                                    group=32, router_bias=bias)
+    x = dev(rng.standard_normal((T, 32)).astype(np.float16))
+    side = torch.cuda.Stream()
+    for a in range(1, 8):
+        part = full[a:]
+        assert part.data_ptr() % 16 or a % 2 == 0
+        ids = torch.empty((T - a, topk), dtype=torch.int32, device="cuda")
+        w = torch.empty((T - a, topk), dtype=torch.float32, device="cuda")
+        torch.cuda.synchronize()
+        sq.sq_moe_route(part, ids, w, bias=bias, stream=side)
+        torch.cuda.synchronize()
+        rid, rw = ref.route(l[a:], topk, host(bias))
+        assert np.array_equal(host(ids), rid)
+        assert (np.abs(host(w) - rw) <= (2.0**-24 + 2.0**-40) * rw).all()
+        assert torch.equal(layer(x[a:], part), layer(x[a:], part.clone()))
+
+
+def test_route_refuses_host_logits_off_16_bytes():
+    import w8a8_int8_linear_channel_b200 as sq
+    l = torch.zeros(3 * 60 + 1, dtype=torch.float16)[1:].view(3, 60)
+    ids, w = torch.zeros((3, 2), dtype=torch.int32), torch.zeros((3, 2))
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        sq.sq_moe_route(l, ids, w)

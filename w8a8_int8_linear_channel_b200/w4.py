@@ -46,6 +46,12 @@ def _stream(stream) -> int:
     return _raw_stream(_current_device()) if stream is None else stream.cuda_stream
 
 
+def _realigned(logits: torch.Tensor, stream=None) -> torch.Tensor:
+    """Rows that start off 16 bytes (a slice of a batch may) copied, contiguous, in the stream's order."""
+    with torch.cuda.stream(stream):
+        return logits.clone(memory_format=torch.contiguous_format)
+
+
 class W4Weight:
     """A packed 4-bit weight [N, K] (or one per expert): the library's buffer and its shape."""
 
@@ -174,7 +180,7 @@ def sq_moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
                  n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
                  scale: float = 1.0, stream=None):
     """The topk experts of every token (ids int32 [T, topk], largest choice first) and their weights
-    (fp32 [T, topk]) from router logits, fp32 or fp16 [T, E]."""
+    (fp32 [T, topk]) from router logits, fp32 or fp16 [T, E] (copied first when they start off 16 bytes)."""
     half = logits.dtype == _F16
     if not half and logits.dtype != _F32:
         raise ValueError("logits: fp32 or fp16")
@@ -195,6 +201,8 @@ def sq_moe_route(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
         _tensor(weights, _F32, shape, "weights")
     if bias is not None:
         _vec(bias, E, _F32, "bias")
+    if logits.data_ptr() % 16:
+        logits, ld = _realigned(logits, stream), E
     dev = logits.get_device()
     if dev < 0 or dev != ids.get_device() or dev != weights.get_device() or (
             bias is not None and dev != bias.get_device()) or dev != _current_device():
@@ -368,6 +376,8 @@ class W4Experts:
         (T, _), (ldx, inner), (ldl, linner) = x2.shape, x2.stride(), l2.stride()
         if inner != 1 or linner != 1:
             raise ValueError("x / logits: need a unit inner stride")
+        if l2.data_ptr() % 16:
+            l2, ldl = _realigned(l2), E
         y = x.new_empty(shape)
         if T == 0:
             return y
