@@ -154,7 +154,7 @@ def sq_w4a16_linear(x: torch.Tensor, w4: W4Weight, y: torch.Tensor, bias=None, r
     N = w4.N
     if K != w4.K or inner != 1:
         raise ValueError(f"x: need [M, {w4.K}] with a unit inner stride, got {tuple(shape)}")
-    if M == 1 and ld < K:
+    if M == 1:
         ld = K  # the stride of a single row means nothing
     if y.dtype != _F16 or y.shape != (M, N) or not y.is_contiguous():
         _tensor(y, _F16, (M, N), "y")
@@ -260,7 +260,7 @@ def sq_w4a16_experts(x: torch.Tensor, w4: W4Weight, offsets: torch.Tensor, order
     if K != w4.K:
         raise ValueError(f"x: need [rows, {w4.K}], got {tuple(x.shape)}")
     if rows == 1:
-        ld = max(ld, K)
+        ld = K
     pairs = order.numel()
     _vec(offsets, w4.experts + 1, torch.int32, "offsets")
     _vec(order, pairs, torch.int32, "order")
