@@ -519,6 +519,9 @@ sq_status sq_moe_plan(const int32_t* ids, int64_t pairs, int64_t E, int32_t* off
  * order not from sq_moe_plan lists twice either result may stay.
  *   x fp16 [rows, ldx]; w4: E packed weights; bias fp16 [E, N] or NULL;
  *   y fp16 [pairs, N], or fp32 with y_f32 != 0
+ * The hidden rows of a feed-forward layer, one product's y and the next one's x,
+ * are fp16 and so rounded once (Inf past 65504); the last product's rows can stay fp32 up to
+ * sq_moe_combine.
  */
 sq_status sq_w4a16_experts(const void* x_f16, int64_t rows, int64_t ldx, const void* w4, int64_t E, int64_t N,
                            int64_t K, int group, int has_zero, const void* bias_f16, int relu,
