@@ -437,7 +437,7 @@ size_t sq_w4_packed_bytes(int64_t N, int64_t K, int group, int has_zero);
  * with zero points, lo = min(w', 0), hi = max(w', 0):
  *   s = fp16( r7( (hi - lo) / 15 ) ),  z = min(rint(-lo / s), 15),
  *   q = clamp(rint(w' / s) + z, 0, 15)
- * where r8 / r7 round to 8 / 7 significant bits, so that every (q - z) * s is
+ * (fp32 steps) where r8 / r7 round to 8 / 7 significant bits, so that every (q - z) * s is
  * exactly an fp16 number (unless it lies past fp16's range, which weights near
  * the type's largest value can come to).  A group of zeros gets scale 0; a NaN never sets a
  * range and is coded as zero; an Inf gives scale Inf (its group's values are
@@ -463,9 +463,9 @@ sq_status sq_w4_dequantize(const void* w4, int64_t N, int64_t K, int group, int 
  * rounding when relu (a NaN becomes 0).  Sums are fp32.  Needs no workspace;
  * the same inputs give the same bits on every call (a row's bits may depend on
  * the number of rows: few and many tokens take different kernels).  With many
- * tokens W is rounded to fp16 once, as sq_w4_dequantize shows it, which changes
+ * tokens W is rounded to fp16 once, as sq_w4_dequantize shows it (Inf past 65504), which changes
  * nothing for weights from sq_quantize_weight_w4 or any scales of 7 significant
- * bits.
+ * bits.  A scale that is Inf or NaN makes its channel's outputs Inf or NaN (before the ReLU).
  *   x fp16 [M, ldx], ldx >= K, ldx % 8 == 0; bias fp16 [N] or NULL; y fp16 [M, N]
  */
 sq_status sq_w4a16_linear(const void* x_f16, int64_t M, int64_t ldx, const void* w4, int64_t N, int64_t K, int group,

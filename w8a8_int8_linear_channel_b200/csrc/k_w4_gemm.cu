@@ -7,7 +7,8 @@
 // memory, from where tcgen05.mma reads its A operand; the tokens (B) are
 // staged in shared memory.  A weight made by the library's quantizer is
 // exactly an fp16 number, so nothing is rounded before the fp32 accumulators
-// (a scale of more than 8 significant bits costs one fp16 rounding per weight).
+// (a scale of more than 8 significant bits, 7 with zero points, costs one fp16
+// rounding per weight, and (q - z) * s past 65504 is Inf).
 //
 // Why tensor memory: writing the 32 KB of a dequantized 128 x 128 tile to
 // shared memory and reading it back as the MMA's operand would take twice the
@@ -26,8 +27,9 @@
 // its end; with one CTA per SM nothing covers the two ends.  For few tokens
 // the chain per K tile is all: 4096 x 16384 at 16 tokens 18.4 us.
 //
-// Tensor memory never has to be waited for: a CTA takes 256 columns and its
-// shared memory lets two of them share an SM, or 512 and one.
+// Tensor memory is not waited for among this kernel's CTAs: one takes 256 columns
+// and its shared memory lets two of them share an SM, or 512 and one.  Beside the INT8
+// products' CTAs (over 190 KB of shared memory) none of them fits.
 #include "sq_tmap.h"
 #include "sq_w4.cuh"
 
@@ -596,12 +598,12 @@ __global__ void __launch_bounds__(Layout<BT, RT, G, ZERO>::THREADS, RT == 2 ? 1 
 
 // Slices of K per weight tile (the cluster size).  A CTA's time is taken as
 // 0.39 us per K tile (0.59 with 128 tokens), 4.5 for start and finish and 4 more
-// for the cluster's sum (4096 x 4096 at 64 tokens: 17.0 us with one slice, 11.5
-// with four, 10.7 by now).  Two CTAs on an SM overlap their tiles, hardly the
-// rest: with clusters until every SM has two, 4096 x 4096 at 384 tokens took
-// 41.1 us, with one slice 26.4 (19.8 by now).  Clusters of more than two do not
-// pack every SM of a GPC; an eighth is taken off (4096 x 16384 at 384 tokens:
-// 288 CTAs in threes 86.7 us, in twos 70.3).
+// for the cluster's sum (4096 x 4096 at 64 tokens: 15.7 us with one slice, 14.6 with
+// two, 10.8 with four; 4096 x 16384 at 16: two 30.5, four 18.6, eight 17.8, four chosen).
+// Two CTAs on an SM overlap their tiles, hardly the rest: 4096 x 4096 at 384 tokens
+// takes 19.8 us with one slice, 29.0 with two.  Clusters of more than two do not
+// pack every SM of a GPC; an eighth is taken off (4096 x 16384 at 384 tokens with
+// one / two / three slices 67.8 / 64.4 / 75.3 us).
 int pick_slices(int64_t units, int64_t kt, int bt, int num_sms) {
   int slices = 1;
   int64_t best = INT64_MAX;

@@ -389,7 +389,10 @@ int64_t w4_blocks(const W4Product& p, int bt) {
 // Experts' tokens scatter around the average (most of them still need one
 // block of eight): 64 experts with 10 tokens each 207 us a layer here and 222
 // there, with 12 242 and 217; 256 small experts with 10 122 and 129, with 16
-// 162 and 130.
+// 162 and 130.  The average is all the host knows.  Where the load is uneven this kernel
+// still holds (64 experts, 640 pairs, half of them on one: a product of 2048 x 4096 91 us here,
+// 99 there), until nearly all pairs meet one expert, whose weight it then reads once per eight (all of them on one:
+// 73 and 37; 512 experts of 512 x 2048, 4096 pairs: evenly 115 and 118, all on one 82 and 52).
 constexpr int kTilesPerSm = 32;    // 64 channels x 128 k x eight tokens
 constexpr int kTokensExperts = 10;
 

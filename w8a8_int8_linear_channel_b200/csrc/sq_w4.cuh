@@ -15,8 +15,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // mbar_wait whose tries suspend the warp (up to 2 us each) instead of polling:
-// with fourteen warps on a scheduler's issue slots the waiting ones must not
-// take any.
+// with up to seven warps on a scheduler (two CTAs of fourteen on an SM) the
+// waiting ones must not take issue slots.
 __device__ __forceinline__ bool w4_wait(uint32_t bar, uint32_t parity, uint64_t budget_ns, uint32_t* status,
                                         volatile uint32_t* abort) {
   if (mbar_try_wait_hint(bar, parity, 2000)) return true;
